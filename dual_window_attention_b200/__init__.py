@@ -11,6 +11,7 @@ call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -127,6 +128,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ttcd_fastweight_mlp_backward_workspace_size.restype = sz
     lib.ttcd_fastweight_mlp_backward.argtypes = [vp, vp, vp, W, P, vp, vp, vp, vp, vp, vp, vp,
                                                  ctypes.POINTER(_MlpGrads), vp, sz, vp]
+    lib.ttcd_sink_window_attn.argtypes = [vp] * 5 + [i] * 7 + [f, i, vp]
+    lib.ttcd_sink_window_attn_backward_workspace_size.argtypes = [i] * 7
+    lib.ttcd_sink_window_attn_backward_workspace_size.restype = sz
+    lib.ttcd_sink_window_attn_backward.argtypes = [vp] * 9 + [i] * 7 + [f, vp, sz, vp]
+    lib.ttcd_paged_kv_append.argtypes = [vp] * 7 + [i] * 8 + [f, i, vp]
+    lib.ttcd_paged_window_attn.argtypes = [vp] * 8 + [i] * 11 + [f, i, vp]
     lib.ttcd_fastweight_mlp_noalloc.argtypes = [vp, vp, vp, vp, W, P, vp, vp, vp, vp]
     lib.ttcd_fastweight_mlp_noalloc.restype = i
     lib.ttcd_fastweight_mlp_noalloc_capacity.argtypes = []
@@ -137,7 +144,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                "ttcd_decode_state_init", "ttcd_block_decode", "ttcd_decode_state_read",
                "ttcd_block_decode_next", "ttcd_block_decode_next_ex", "ttcd_fastweight_mlp_backward",
                "ttcd_dual_window_attn_backward", "ttcd_block_backward",
-               "ttcd_shard_qkv", "ttcd_shard_attend", "ttcd_shard_mix", "ttcd_shard_finish"):
+               "ttcd_shard_qkv", "ttcd_shard_attend", "ttcd_shard_mix", "ttcd_shard_finish",
+               "ttcd_sink_window_attn", "ttcd_sink_window_attn_backward", "ttcd_paged_kv_append",
+               "ttcd_paged_window_attn"):
         getattr(lib, fn).restype = i
     _lib = lib
     return lib
@@ -697,6 +706,166 @@ def fastweight_mlp_noalloc(u_T, u_S, beta, weights: Dict[str, torch.Tensor], p: 
                                          _ptr(state_out), _ptr(y), _stream(stream))
     _check(st, "ttcd_fastweight_mlp_noalloc")
     return y, state_out
+
+
+def _launching(device: torch.device, stream):
+    """Makes the tensors' device and the call's stream current, so that what the
+    call allocates belongs to the stream that uses it."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _takes(what: str, device, **tensors) -> None:
+    """Refuses a tensor of another shape, type or device than the call takes:
+    ``name=(tensor, shape, dtypes)``."""
+    if device.type != "cuda":
+        raise ValueError(f"{what}: libttcd takes CUDA tensors only (no CPU path)")
+    for name, (t, shape, dtypes) in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{what}: {name} is on {t.device}, not on {device}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{what}: {name} is {t.dtype}")
+
+
+_F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
+_ACT = (torch.bfloat16, torch.float32)  # fp32 activations: the library says unsupported
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return BF16 if t.dtype == torch.bfloat16 else F32
+
+
+def sink_window_attn(q, k, v, window: int, n_sink: int, scale: float = 0.0, o=None,
+                     lse: bool = False, stream=None):
+    """Sliding-window attention whose first ``n_sink`` tokens stay visible: the
+    query at t sees key j iff j <= t and (j > t - window or j < n_sink).
+    q [B, T, Hq, hd], k and v [B, T, Hkv, hd] bf16, hd 32, 64 or 128.
+    Returns (o, lse [B, Hq, T] or None)."""
+    lib = load_library()
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("sink_window_attn: q and k are [B, T, heads, head_dim]")
+    B, T, Hq, hd = q.shape
+    Hkv = k.shape[2]
+    _takes("sink_window_attn", q.device, q=(q, q.shape, _ACT), k=(k, (B, T, Hkv, hd), (q.dtype,)),
+           v=(v, (B, T, Hkv, hd), (q.dtype,)), o=(o, q.shape, (q.dtype,)))
+    with _launching(q.device, stream):
+        o = torch.empty_like(q) if o is None else o
+        ls = torch.empty(B, Hq, T, device=q.device, dtype=torch.float32) if lse else None
+        _check(lib.ttcd_sink_window_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(ls), B, T, Hq,
+                                         Hkv, hd, window, n_sink, scale, _dtype_code(q),
+                                         _stream(None)), "ttcd_sink_window_attn")
+    return o, ls
+
+
+def sink_window_attn_backward(q, k, v, o, lse, d_o, window: int, n_sink: int, scale: float = 0.0,
+                              workspace: Optional[torch.Tensor] = None, stream=None):
+    """Vector-Jacobian product of ``sink_window_attn`` (bf16, hd 64 or 128):
+    (dq, dk, dv) in bf16 for the output gradient d_o, given the forward's o and
+    lse.  Returns (dq, dk, dv, workspace)."""
+    lib = load_library()
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("sink_window_attn_backward: q and k are [B, T, heads, head_dim]")
+    B, T, Hq, hd = q.shape
+    Hkv = k.shape[2]
+    kv = (B, T, Hkv, hd)
+    _takes("sink_window_attn_backward", q.device, q=(q, q.shape, _BF16), k=(k, kv, _BF16),
+           v=(v, kv, _BF16), o=(o, q.shape, _BF16), lse=(lse, (B, Hq, T), _F32),
+           d_o=(d_o, q.shape, _BF16))
+    with _launching(q.device, stream):
+        if workspace is None:
+            need = int(lib.ttcd_sink_window_attn_backward_workspace_size(B, T, Hq, Hkv, hd, window,
+                                                                         n_sink))
+            workspace = alloc_workspace(need, q.device)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        _check(lib.ttcd_sink_window_attn_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk),
+            _ptr(dv), B, T, Hq, Hkv, hd, window, n_sink, scale, _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(None)),
+            "ttcd_sink_window_attn_backward")
+    return dq, dk, dv, workspace
+
+
+def _paged(what: str, device, k_pages, v_pages, block_table, q_start, kv_len, hd: int):
+    """The checked sizes of a paged cache and its ragged batch: (n_seq, n_pages,
+    page_size, max_pages, Hkv)."""
+    if k_pages.dim() != 4 or block_table.dim() != 2 or kv_len.dim() != 1:
+        raise ValueError(f"{what}: k_pages is [n_pages, Hkv, page_size, head_dim], block_table "
+                         "[n_seq, max_pages], kv_len [n_seq]")
+    n_pages, Hkv, page_size, _ = k_pages.shape
+    n_seq, max_pages = block_table.shape
+    pages = (n_pages, Hkv, page_size, hd)
+    _takes(what, device, k_pages=(k_pages, pages, _ACT), v_pages=(v_pages, pages, (k_pages.dtype,)),
+           block_table=(block_table, (n_seq, max_pages), _I32), q_start=(q_start, (n_seq + 1,), _I32),
+           kv_len=(kv_len, (n_seq,), _I32))
+    return n_seq, n_pages, page_size, max_pages, Hkv
+
+
+def paged_kv_append(qkv, k_pages, v_pages, block_table, q_start, kv_len, n_q_heads: int,
+                    rope_theta: float = 10000.0, q=None, stream=None):
+    """New tokens into a paged cache: q and k of the projected rows ``qkv``
+    [total, (Hq + 2 Hkv) hd] get their rotary positions, k and v go to their
+    pages (in place).  ``block_table`` [n_seq, max_pages], ``q_start`` [n_seq + 1]
+    and ``kv_len`` [n_seq] (with the new tokens) are int32 on the device.
+    Returns the rotated q [total, Hq, hd] (``q`` when given, whose padding rows
+    are left as they were)."""
+    lib = load_library()
+    if k_pages.dim() != 4 or qkv.dim() != 2:
+        raise ValueError("paged_kv_append: qkv is [total, (Hq + 2 Hkv) head_dim], k_pages "
+                         "[n_pages, Hkv, page_size, head_dim]")
+    hd = k_pages.shape[3]
+    n_seq, n_pages, page_size, max_pages, Hkv = _paged(
+        "paged_kv_append", qkv.device, k_pages, v_pages, block_table, q_start, kv_len, hd)
+    total = qkv.shape[0]
+    _takes("paged_kv_append", qkv.device,
+           qkv=(qkv, (total, (n_q_heads + 2 * Hkv) * hd), (k_pages.dtype,)),
+           q=(q, (total, n_q_heads, hd), (qkv.dtype,)))
+    with _launching(qkv.device, stream):
+        if q is None:
+            q = torch.empty(total, n_q_heads, hd, device=qkv.device, dtype=qkv.dtype)
+        _check(lib.ttcd_paged_kv_append(_ptr(qkv), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+                                        _ptr(block_table), _ptr(q_start), _ptr(kv_len), n_seq,
+                                        total, n_pages, page_size, max_pages, n_q_heads, Hkv, hd,
+                                        rope_theta, _dtype_code(qkv), _stream(None)),
+               "ttcd_paged_kv_append")
+    return q
+
+
+def paged_window_attn(q, k_pages, v_pages, block_table, q_start, kv_len, window: int, n_sink: int,
+                      max_q: int, scale: float = 0.0, o=None, lse=False, stream=None):
+    """Attention of new tokens' queries q [total, Hq, hd] over a paged cache, with
+    the mask of ``sink_window_attn`` at the tokens' positions; their own k and v
+    are in the cache already (``paged_kv_append``).  ``max_q``: about the most new
+    tokens of any sequence (it chooses the kernel).  ``lse``: True, or a tensor
+    [Hq, total] to write.  Returns (o, lse or None)."""
+    lib = load_library()
+    if q.dim() != 3:
+        raise ValueError("paged_window_attn: q is [total, Hq, head_dim]")
+    total, Hq, hd = q.shape
+    n_seq, n_pages, page_size, max_pages, Hkv = _paged(
+        "paged_window_attn", q.device, k_pages, v_pages, block_table, q_start, kv_len, hd)
+    given = lse if isinstance(lse, torch.Tensor) else None
+    _takes("paged_window_attn", q.device, q=(q, q.shape, (k_pages.dtype,)),
+           o=(o, q.shape, (q.dtype,)), lse=(given, (Hq, total), _F32))
+    with _launching(q.device, stream):
+        o = torch.empty_like(q) if o is None else o
+        ls = given
+        if ls is None and lse is True:
+            ls = torch.empty(Hq, total, device=q.device, dtype=torch.float32)
+        _check(lib.ttcd_paged_window_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
+                                          _ptr(q_start), _ptr(kv_len), _ptr(o), _ptr(ls), n_seq,
+                                          total, max_q, n_pages, page_size, max_pages, Hq, Hkv,
+                                          hd, window, n_sink, scale, _dtype_code(q),
+                                          _stream(None)), "ttcd_paged_window_attn")
+    return o, ls
 
 
 def check_device_status(workspace: torch.Tensor, stream=None) -> int:

@@ -14,6 +14,7 @@ namespace ttcd {
 enum : uint32_t {
   DEV_ERR_TIMEOUT = 1u,        // a bounded wait gave up
   DEV_ERR_BAD_LAUNCH = 2u,     // a kernel found its launch geometry inconsistent
+  DEV_ERR_BAD_INDEX = 4u,      // a paged call met a page or a length that cannot be
 };
 
 struct DevStatus {

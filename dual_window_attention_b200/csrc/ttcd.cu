@@ -22,6 +22,8 @@
 #include "decode.cuh"
 #include "backward.cuh"
 #include "attention_bwd.cuh"
+#include "sink_attention.cuh"
+#include "paged_append.cuh"
 
 using namespace ttcd;
 
@@ -827,6 +829,7 @@ ttcd_status read_clear_status(uint32_t* word, cudaStream_t s, uint32_t* flags) {
   if (v && cudaMemsetAsync(word, 0, sizeof(v), s) != cudaSuccess) return TTCD_ERR_CUDA;
   if (flags) *flags = v;
   if (v & DEV_ERR_TIMEOUT) return TTCD_ERR_TIMEOUT;
+  if (v & DEV_ERR_BAD_INDEX) return TTCD_ERR_INVALID_ARG;
   return v ? TTCD_ERR_CUDA : TTCD_OK;
 }
 
@@ -2643,6 +2646,209 @@ ttcd_status ttcd_block_backward(const void* x, const float* beta, const ttcd_blo
   return block_backward_bf16(c, static_cast<const bf*>(x), beta, w, p, state_in,
                              static_cast<const bf*>(d_out), d_state_out, dx, d_beta, d_state_in,
                              grads, workspace, L);
+}
+
+}  // extern "C"
+
+// ================================================================== windows with sinks
+// Sliding-window attention with sinks over dense sequences (forward, backward)
+// and over a paged cache, and the write of new tokens into that cache.
+namespace {
+
+constexpr int kMaxSinks = 128;  // the sinks lie in the first tile of 128 keys
+
+ttcd_status check_sink_shape(int Hq, int Hkv, int hd, int window, int n_sink, float scale,
+                             ttcd_dtype dtype) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || window < 1 || n_sink < 0 || !(scale >= 0.f) ||
+      !std::isfinite(scale))
+    return TTCD_ERR_INVALID_ARG;
+  if (dtype != TTCD_BF16) return dtype == TTCD_F32 ? TTCD_ERR_UNSUPPORTED : TTCD_ERR_INVALID_ARG;
+  if (hd != 32 && hd != 64 && hd != 128) return TTCD_ERR_UNSUPPORTED;
+  if (n_sink > kMaxSinks || Hq / Hkv > 128) return TTCD_ERR_UNSUPPORTED;
+  return TTCD_OK;
+}
+bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+int log2_of(int n) {
+  int l = 0;
+  while ((1 << l) < n) ++l;
+  return l;
+}
+// Sizes of a paged call.
+ttcd_status check_paged_shape(int n_seq, int total_q, int n_pages, int page_size, int max_pages,
+                              int Hkv) {
+  if (n_seq < 1 || total_q < 1 || n_pages < 1 || max_pages < 1 || page_size < 1)
+    return TTCD_ERR_INVALID_ARG;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    return TTCD_ERR_UNSUPPORTED;
+  // rows of the cache and positions of a sequence are 32-bit
+  if (static_cast<long long>(n_pages) * page_size * Hkv >= (1ll << 31) - 128 ||
+      static_cast<long long>(max_pages) * page_size >= (1ll << 30) || total_q >= (1 << 30) ||
+      n_seq >= (1 << 30))
+    return TTCD_ERR_UNSUPPORTED;
+  return TTCD_OK;
+}
+int clamp_window(int window) { return window < (1 << 30) ? window : (1 << 30); }
+
+template <int HD, bool PAGED>
+ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const void* v,
+                            const PagedCache& pc, const Ragged& rg, void* o, float* lse, int B,
+                            int T, int Hq, int Hkv, int window, int n_sink, float scale) {
+  using bf = __nv_bfloat16;
+  const long long items = (PAGED ? static_cast<long long>(rg.total_q) : static_cast<long long>(B) * T) * Hq;
+  sink_attn_simple_kernel<HD, PAGED><<<static_cast<unsigned>(cdiv(items, 8)), 256, 0, c.s>>>(
+      static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v), pc, rg,
+      static_cast<bf*>(o), lse, B, T, Hq, Hkv, window, n_sink, scale, c.st.err);
+  TTCD_CHECK_LAUNCH();
+  return TTCD_OK;
+}
+
+template <int HD>
+ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const void* v,
+                            const void* o, const float* lse, const void* d_o, void* dq, void* dk,
+                            void* dv, int B, int T, int Hq, int Hkv, int window, int n_sink,
+                            float scale) {
+  using bf = __nv_bfloat16;
+  const bf *q_ = static_cast<const bf*>(q), *k_ = static_cast<const bf*>(k),
+           *v_ = static_cast<const bf*>(v), *o_ = static_cast<const bf*>(o),
+           *g_ = static_cast<const bf*>(d_o);
+  const long long BT = static_cast<long long>(B) * T;
+  sink_attn_dq_simple_kernel<HD><<<static_cast<unsigned>(cdiv(BT * Hq, 8)), 256, 0, c.s>>>(
+      q_, k_, v_, o_, lse, g_, static_cast<bf*>(dq), B, T, Hq, Hkv, window, n_sink, scale);
+  TTCD_CHECK_LAUNCH();
+  sink_attn_dkv_simple_kernel<HD><<<static_cast<unsigned>(cdiv(BT * Hkv, 8)), 256, 0, c.s>>>(
+      q_, k_, v_, o_, lse, g_, static_cast<bf*>(dk), static_cast<bf*>(dv), B, T, Hq, Hkv, window,
+      n_sink, scale);
+  TTCD_CHECK_LAUNCH();
+  return TTCD_OK;
+}
+
+size_t sink_bwd_ws_bytes(int B, int T, int Hq, int Hkv, int hd, int window, int n_sink) {
+  (void)B; (void)T; (void)Hq; (void)Hkv; (void)hd; (void)window; (void)n_sink;
+  return kStatusBytes;
+}
+ttcd_status check_sink_bwd(int B, int T, int Hq, int Hkv, int hd, int window, int n_sink) {
+  if (B < 1 || T < 1) return TTCD_ERR_INVALID_ARG;
+  TTCD_TRY(check_sink_shape(Hq, Hkv, hd, window, n_sink, 0.f, TTCD_BF16));
+  if (hd == 32) return TTCD_ERR_UNSUPPORTED;
+  // rows of (token, head) and tokens are 32-bit
+  if (static_cast<long long>(B) * T * Hq >= (1ll << 31) - 128 || T >= (1 << 30))
+    return TTCD_ERR_UNSUPPORTED;
+  return TTCD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ttcd_status ttcd_sink_window_attn(const void* q, const void* k, const void* v, void* o,
+                                  float* lse, int B, int T, int Hq, int Hkv, int hd, int window,
+                                  int n_sink, float scale, ttcd_dtype dtype, void* stream) {
+  if (B < 1 || T < 1) return TTCD_ERR_INVALID_ARG;
+  TTCD_TRY(check_sink_shape(Hq, Hkv, hd, window, n_sink, scale, dtype));
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || (lse && !aligned16(lse)))
+    return TTCD_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * T >= (1ll << 31) - 128 || T >= (1 << 30))
+    return TTCD_ERR_UNSUPPORTED;
+  Ctx c;
+  TTCD_TRY(make_ctx(stream, c));
+  const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(hd));
+  const int w = clamp_window(window);
+  const PagedCache pc{};
+  const Ragged rg{};
+  switch (hd) {
+    case 32: return launch_sink_fwd<32, false>(c, q, k, v, pc, rg, o, lse, B, T, Hq, Hkv, w, n_sink, sc);
+    case 64: return launch_sink_fwd<64, false>(c, q, k, v, pc, rg, o, lse, B, T, Hq, Hkv, w, n_sink, sc);
+    default: return launch_sink_fwd<128, false>(c, q, k, v, pc, rg, o, lse, B, T, Hq, Hkv, w, n_sink, sc);
+  }
+}
+
+size_t ttcd_sink_window_attn_backward_workspace_size(int B, int T, int Hq, int Hkv, int hd,
+                                                     int window, int n_sink) {
+  if (check_sink_bwd(B, T, Hq, Hkv, hd, window, n_sink) != TTCD_OK) return 0;
+  return sink_bwd_ws_bytes(B, T, Hq, Hkv, hd, clamp_window(window), n_sink);
+}
+
+ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const void* v,
+                                           const void* o, const float* lse, const void* d_o,
+                                           void* dq, void* dk, void* dv, int B, int T, int Hq,
+                                           int Hkv, int hd, int window, int n_sink, float scale,
+                                           void* workspace, size_t ws_bytes, void* stream) {
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return TTCD_ERR_INVALID_ARG;
+  TTCD_TRY(check_sink_bwd(B, T, Hq, Hkv, hd, window, n_sink));
+  const void* need[] = {q, k, v, o, lse, d_o, dq, dk, dv, workspace};
+  for (const void* x : need)
+    if (!aligned16(x)) return TTCD_ERR_INVALID_ARG;
+  const int w = clamp_window(window);
+  if (ws_bytes < sink_bwd_ws_bytes(B, T, Hq, Hkv, hd, w, n_sink)) return TTCD_ERR_WORKSPACE;
+  Ctx c;
+  TTCD_TRY(make_ctx(stream, c, workspace));
+  const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(hd));
+  if (hd == 64)
+    return launch_sink_bwd<64>(c, q, k, v, o, lse, d_o, dq, dk, dv, B, T, Hq, Hkv, w, n_sink, sc);
+  return launch_sink_bwd<128>(c, q, k, v, o, lse, d_o, dq, dk, dv, B, T, Hq, Hkv, w, n_sink, sc);
+}
+
+ttcd_status ttcd_paged_kv_append(const void* qkv, void* q_out, void* k_pages, void* v_pages,
+                                 const int* block_table, const int* q_start, const int* kv_len,
+                                 int n_seq, int total_q, int n_pages, int page_size,
+                                 int max_pages, int Hq, int Hkv, int hd, float rope_theta,
+                                 ttcd_dtype dtype, void* stream) {
+  TTCD_TRY(check_sink_shape(Hq, Hkv, hd, 1, 0, 0.f, dtype));
+  TTCD_TRY(check_paged_shape(n_seq, total_q, n_pages, page_size, max_pages, Hkv));
+  if (!(rope_theta >= 0.f) || !std::isfinite(rope_theta)) return TTCD_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned4(block_table) || !aligned4(q_start) || !aligned4(kv_len))
+    return TTCD_ERR_INVALID_ARG;
+  Ctx c;
+  TTCD_TRY(make_ctx(stream, c));
+  using bf = __nv_bfloat16;
+  AppendArgs a;
+  a.qkv = static_cast<const bf*>(qkv);
+  a.q_out = static_cast<bf*>(q_out);
+  a.k_pages = static_cast<bf*>(k_pages);
+  a.v_pages = static_cast<bf*>(v_pages);
+  a.table = block_table;
+  a.rg = Ragged{q_start, kv_len, n_seq, total_q};
+  a.max_pages = max_pages;
+  a.n_pages = n_pages;
+  a.page_log2 = log2_of(page_size);
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.hd = hd;
+  a.rotate = rope_theta > 0.f;
+  a.log2_theta = a.rotate ? std::log2(static_cast<double>(rope_theta)) : 0.0;
+  const int blocks = std::min(total_q, c.sms * 8);
+  paged_append_kernel<1><<<static_cast<unsigned>(blocks), APPEND_THREADS, 0, c.s>>>(a, c.st.err);
+  TTCD_CHECK_LAUNCH();
+  return TTCD_OK;
+}
+
+ttcd_status ttcd_paged_window_attn(const void* q, const void* k_pages, const void* v_pages,
+                                   const int* block_table, const int* q_start, const int* kv_len,
+                                   void* o, float* lse, int n_seq, int total_q, int max_q,
+                                   int n_pages, int page_size, int max_pages, int Hq, int Hkv,
+                                   int hd, int window, int n_sink, float scale, ttcd_dtype dtype,
+                                   void* stream) {
+  TTCD_TRY(check_sink_shape(Hq, Hkv, hd, window, n_sink, scale, dtype));
+  TTCD_TRY(check_paged_shape(n_seq, total_q, n_pages, page_size, max_pages, Hkv));
+  if (max_q < 1) return TTCD_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
+      (lse && !aligned16(lse)) || !aligned4(block_table) || !aligned4(q_start) ||
+      !aligned4(kv_len))
+    return TTCD_ERR_INVALID_ARG;
+  Ctx c;
+  TTCD_TRY(make_ctx(stream, c));
+  using bf = __nv_bfloat16;
+  const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(hd));
+  const int w = clamp_window(window);
+  const PagedCache pc{static_cast<const bf*>(k_pages), static_cast<const bf*>(v_pages), block_table,
+                      max_pages, n_pages, log2_of(page_size), Hkv};
+  const Ragged rg{q_start, kv_len, n_seq, total_q};
+  switch (hd) {
+    case 32: return launch_sink_fwd<32, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, Hkv, w, n_sink, sc);
+    case 64: return launch_sink_fwd<64, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, Hkv, w, n_sink, sc);
+    default: return launch_sink_fwd<128, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, Hkv, w, n_sink, sc);
+  }
 }
 
 }  // extern "C"

@@ -38,8 +38,8 @@
  *     it accumulates over calls until ttcd_check_device_status() reads and
  *     clears it, so zero the first TTCD_STATUS_BYTES bytes of a new workspace
  *     before its first use (ttcd_decode_state_init clears a decode state).
- *     Entry points without a workspace (the two attention calls and
- *     ttcd_fastweight_mlp_noalloc) record into one status word per device,
+ *     Entry points without a workspace (the attention forwards, the paged calls
+ *     and ttcd_fastweight_mlp_noalloc) record into one status word per device,
  *     shared by all their callers and read by ttcd_get_device_error().
  */
 #ifndef TTCD_H_
@@ -558,6 +558,109 @@ ttcd_status ttcd_block_decode_next_ex(const void* x_t, const float* beta_t,
                                       void* state, size_t state_bytes, void* y, void* workspace,
                                       size_t ws_bytes, int commit, void* stream);
 
+/*
+ * Sliding-window attention with sinks.
+ *
+ * A sliding window forgets the first tokens of a sequence, on which a trained
+ * softmax leans when nothing in the window matters; keeping a few of them
+ * visible lets a stream run past the window.  The mask of every entry point
+ * below: the query at position t sees key j iff
+ *   j <= t  and  (j > t - window  or  j < n_sink).
+ * The query sees itself, so no row is empty.  One window per call: the teacher
+ * and the student window of a block are two calls (the student window is a
+ * small part of the work).  window >= 1 (larger than the sequence: causal),
+ * 0 <= n_sink <= 128, Hq / Hkv <= 128.
+ *
+ * ttcd_sink_window_attn: dense sequences.
+ *   o[t,h] = sum_j p_j v[j,g],  p = softmax_j(scale q[t,h].k[j,g]) over the mask
+ *   q          [B, T, Hq, hd]  bf16, device
+ *   k, v       [B, T, Hkv, hd] bf16, device
+ *   o          [B, T, Hq, hd]  bf16, device, written
+ *   lse        [B, Hq, T] fp32 natural-log log-sum-exp, device, nullable
+ *   scale      softmax scale; 0 => 1/sqrt(hd)
+ *   dtype      must be TTCD_BF16 (TTCD_F32 -> TTCD_ERR_UNSUPPORTED)
+ * ttcd_sink_window_attn_backward: its vector-Jacobian product for dL/do = d_o,
+ *   with the formulas of ttcd_dual_window_attn_backward; hd 64 or 128 (32:
+ *   TTCD_ERR_UNSUPPORTED).  P is rebuilt from the forward's lse.
+ *   o, lse     the forward's outputs
+ *   d_o        [B, T, Hq, hd] bf16, device
+ *   dq         [B, T, Hq, hd]  bf16, device, written
+ *   dk, dv     [B, T, Hkv, hd] bf16, device, written
+ *   workspace  >= ttcd_sink_window_attn_backward_workspace_size(...) bytes,
+ *              device, 16-byte aligned; status word first
+ * Precision: bf16 tensor-core operands, fp32 sums, statistics and exponentials;
+ * P (and dS in the backward) are rounded to bf16 once, as operands; o, dq, dk
+ * and dv are rounded to bf16 once, at the end.  K and V (and in the backward Q
+ * and d_o) are expected finite: rows that no query of a tile sees are not
+ * multiplied, but a non-finite V row also reaches the queries of the same tile
+ * of 128 rows whose mask hides it (their weight for it is 0).
+ * Timeouts of ttcd_sink_window_attn are recorded in the per-device status word.
+ */
+ttcd_status ttcd_sink_window_attn(const void* q, const void* k, const void* v, void* o,
+                                  float* lse, int B, int T, int Hq, int Hkv, int hd, int window,
+                                  int n_sink, float scale, ttcd_dtype dtype, void* stream);
+/* Workspace bytes of the backward; 0 for sizes it does not take. */
+size_t ttcd_sink_window_attn_backward_workspace_size(int B, int T, int Hq, int Hkv, int hd,
+                                                     int window, int n_sink);
+ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const void* v,
+                                           const void* o, const float* lse, const void* d_o,
+                                           void* dq, void* dk, void* dv, int B, int T, int Hq,
+                                           int Hkv, int hd, int window, int n_sink, float scale,
+                                           void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Paged cache: K and V of many sequences in pages of one pool, and the
+ * attention of new tokens over it (one token of a sequence, a chunk of a
+ * prompt, or a batch of both).
+ *
+ *   k_pages, v_pages [n_pages, Hkv, page_size, hd] bf16, device; page_size 16,
+ *                    32, 64 or 128; a page's rows of one head are contiguous
+ *   block_table      [n_seq, max_pages] int32, device: page of the keys
+ *                    [i page_size, (i + 1) page_size) of sequence s
+ *   q_start          [n_seq + 1] int32, device, ascending from 0: the rows of
+ *                    sequence s in the packed new tokens (it may have none);
+ *                    rows from q_start[n_seq] to total_q are padding: not read
+ *                    for any result, and left as they were in every output
+ *   kv_len           [n_seq] int32, device: keys of sequence s with its new
+ *                    tokens; row i of its n has position kv_len - n + i
+ * The four are read on the device, so a captured call can be replayed with
+ * other lengths and pages (its total_q, n_seq and max_pages are the graph's).
+ *
+ * ttcd_paged_kv_append: rotary positions on the new tokens' q and k (rotate
+ *   half, angle position * theta^(-2i/hd)), and their k and v into the cache.
+ *   qkv          [total_q, (Hq + 2 Hkv) hd] bf16, device: q heads, k heads,
+ *                v heads (the rows of x W_qkv^T)
+ *   q_out        [total_q, Hq, hd] bf16, device, written
+ *   k_pages, v_pages  written at the new tokens' positions only
+ *   rope_theta   base; 0: no rotation
+ *   Angles are formed in 64 bits; q and k are rounded to bf16 once.
+ * ttcd_paged_window_attn: the new tokens' queries over the cache, with the mask
+ *   above; the tokens' own k and v must be in the cache (appended before).
+ *   q, o         [total_q, Hq, hd] bf16, device; o written
+ *   lse          [Hq, total_q] fp32, device, nullable
+ *   max_q        >= 1: about the most new tokens of any sequence; it chooses the
+ *                kernel, and results hold whatever it is
+ *   Pages that no new token sees (between the sinks and the window) are never
+ *   read: their table entries may hold anything.  hd 32, 64 or 128.
+ * A table entry outside [0, n_pages) that is needed, or lengths that cannot be
+ * (kv_len below the new tokens or above max_pages page_size, q_start not
+ * ascending or beyond total_q) are recorded in the per-device status word
+ * (ttcd_get_device_error: TTCD_ERR_INVALID_ARG): such a page counts as zeros
+ * and is not written, such a sequence is skipped.  Sequences may share pages
+ * that none of them writes.  Precision as ttcd_sink_window_attn.
+ */
+ttcd_status ttcd_paged_kv_append(const void* qkv, void* q_out, void* k_pages, void* v_pages,
+                                 const int* block_table, const int* q_start, const int* kv_len,
+                                 int n_seq, int total_q, int n_pages, int page_size,
+                                 int max_pages, int Hq, int Hkv, int hd, float rope_theta,
+                                 ttcd_dtype dtype, void* stream);
+ttcd_status ttcd_paged_window_attn(const void* q, const void* k_pages, const void* v_pages,
+                                   const int* block_table, const int* q_start, const int* kv_len,
+                                   void* o, float* lse, int n_seq, int total_q, int max_q,
+                                   int n_pages, int page_size, int max_pages, int Hq, int Hkv,
+                                   int hd, int window, int n_sink, float scale, ttcd_dtype dtype,
+                                   void* stream);
+
 /* Workspace bytes needed by each entry point; 0 if the parameters are invalid. */
 size_t ttcd_fastweight_mlp_workspace_size(const ttcd_block_params* p);
 size_t ttcd_block_forward_workspace_size(const ttcd_block_params* p);
@@ -605,7 +708,8 @@ ttcd_status ttcd_check_device_status(void* workspace, void* stream);
  * workspace (the attention calls, ttcd_fastweight_mlp_noalloc, and
  * ttcd_test_bounded_wait with no status region), on the current device
  * (synchronises `stream`).  *flags receives the raw bits; returns
- * TTCD_ERR_TIMEOUT if a wait gave up since the last read, TTCD_OK otherwise.
+ * TTCD_ERR_TIMEOUT if a wait gave up since the last read, TTCD_ERR_INVALID_ARG
+ * if a paged call met a page or lengths that cannot be, TTCD_OK otherwise.
  * Callers of those entry points share this word. */
 ttcd_status ttcd_get_device_error(uint32_t* flags, void* stream);
 
