@@ -1,5 +1,5 @@
-// Sliding-window attention with sinks (the first n_sink tokens stay visible),
-// dense and over a paged cache, and the write of new tokens into that cache.
+// Sliding-window attention with sinks (the first n_sink tokens stay visible):
+// what its kernels share, dense and over a paged cache.
 #pragma once
 #include "paged_index.h"
 #include "ptx.cuh"
@@ -68,85 +68,6 @@ __device__ __forceinline__ float warp_dot(const float (&a)[HD / 32], const float
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
-}
-
-// One warp per (query row, head), online softmax over the visible keys in fp32.
-template <int HD, bool PAGED>
-__global__ void sink_attn_simple_kernel(const __nv_bfloat16* q, const __nv_bfloat16* kd,
-                                        const __nv_bfloat16* vd, PagedCache pc, Ragged rg,
-                                        __nv_bfloat16* o, float* lse, int B, int T, int Hq,
-                                        int Hkv, int window, int n_sink, float scale,
-                                        uint32_t* err) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int rows = PAGED ? rg.total_q : B * T;
-  if (PAGED && blockIdx.x == 0)  // every sequence's numbers are consistent, or this call says so
-    for (int i = threadIdx.x; i < rg.n_seq; i += blockDim.x)
-      if (load_span(rg, i, static_cast<long long>(pc.max_pages) << pc.page_log2).bad)
-        atomicOr(err, DEV_ERR_BAD_INDEX);
-  if (item >= static_cast<long long>(rows) * Hq) return;
-  const int row = static_cast<int>(item / Hq), h = static_cast<int>(item % Hq);
-  const int g = h / (Hq / Hkv);
-  int t, s = 0;
-  if (PAGED) {
-    int lo = -1;
-    for (int i = 0; i < rg.n_seq; ++i)
-      if (rg.q_start[i] <= row) lo = i;
-    if (lo < 0) return;
-    s = lo;
-    const SeqSpan sp = load_span(rg, s, static_cast<long long>(pc.max_pages) << pc.page_log2);
-    if (sp.bad && lane == 0) atomicOr(err, DEV_ERR_BAD_INDEX);
-    if (row - sp.q0 >= sp.n) return;
-    t = sp.L - sp.n + row - sp.q0;
-  } else {
-    s = row / T;
-    t = row % T;
-  }
-  float qf[E], acc[E] = {};
-  ld_lane<HD>(q + item * HD, lane, qf);
-  float m = -INFINITY, l = 0.f;
-  const KeyRange kr = key_range(t, t, window, n_sink);
-  for (int j = 0; j <= kr.hi; ++j) {
-    if (j == kr.sink_end && j < kr.lo) j = kr.lo;
-    const __nv_bfloat16 *kp, *vp;
-    if (PAGED) {
-      const int id = pc.table[static_cast<long long>(s) * pc.max_pages + (j >> pc.page_log2)];
-      const long long r0 = page_row(id, pc.n_pages, Hkv, g, 1 << pc.page_log2);
-      if (r0 < 0) {
-        if (lane == 0) atomicOr(err, DEV_ERR_BAD_INDEX);
-        kp = vp = nullptr;
-      } else {
-        const long long off = (r0 + (j & ((1 << pc.page_log2) - 1))) * HD;
-        kp = pc.k + off;
-        vp = pc.v + off;
-      }
-    } else {
-      const long long off = ((static_cast<long long>(s) * T + j) * Hkv + g) * HD;
-      kp = kd + off;
-      vp = vd + off;
-    }
-    float kf[E] = {}, vf[E] = {};
-    if (kp) {
-      ld_lane<HD>(kp, lane, kf);
-      ld_lane<HD>(vp, lane, vf);
-    }
-    const float x = warp_dot<HD>(qf, kf) * scale;
-    const float mn = fmaxf(m, x);
-    const float a = __expf(m - mn), e = __expf(x - mn);
-    l = l * a + e;
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = acc[i] * a + e * vf[i];
-    m = mn;
-  }
-  const float inv = 1.f / l;
-#pragma unroll
-  for (int i = 0; i < E; ++i) o[item * HD + lane * E + i] = __float2bfloat16_rn(acc[i] * inv);
-  if (lse && lane == 0) {
-    const long long li = PAGED ? static_cast<long long>(h) * rg.total_q + row
-                               : (static_cast<long long>(s) * Hq + h) * T + t;
-    lse[li] = m + logf(l);
-  }
 }
 
 // Backward, one warp per (query row, head): dq.

@@ -23,6 +23,7 @@
 #include "backward.cuh"
 #include "attention_bwd.cuh"
 #include "sink_attention.cuh"
+#include "sink_attention_fwd.cuh"
 #include "paged_append.cuh"
 
 using namespace ttcd;
@@ -2689,15 +2690,101 @@ ttcd_status check_paged_shape(int n_seq, int total_q, int n_pages, int page_size
 }
 int clamp_window(int window) { return window < (1 << 30) ? window : (1 << 30); }
 
+// bf16 tensor map of any rank with boxes 128 bytes wide, 128-byte swizzle; parts
+// of a box outside the tensor read as zeros.  strides: bytes, of dimensions 1 ...
+bool make_map_nd(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs that share one work unit's keys (a cluster): as many as fill the SMs
+// when the work units alone do not, at least two key tiles each.
+int pick_splits(long long units, int sms, long long key_tiles) {
+  long long s = sms / std::max<long long>(units, 1);
+  s = std::min<long long>(s, key_tiles / 2);
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(s, 8)));
+}
+
 template <int HD, bool PAGED>
 ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const void* v,
                             const PagedCache& pc, const Ragged& rg, void* o, float* lse, int B,
                             int T, int Hq, int Hkv, int window, int n_sink, float scale) {
   using bf = __nv_bfloat16;
-  const long long items = (PAGED ? static_cast<long long>(rg.total_q) : static_cast<long long>(B) * T) * Hq;
-  sink_attn_simple_kernel<HD, PAGED><<<static_cast<unsigned>(cdiv(items, 8)), 256, 0, c.s>>>(
-      static_cast<const bf*>(q), static_cast<const bf*>(k), static_cast<const bf*>(v), pc, rg,
-      static_cast<bf*>(o), lse, B, T, Hq, Hkv, window, n_sink, scale, c.st.err);
+  const int G = Hq / Hkv, tpt = ATT_BM / G;
+  const cuuint64_t rows = PAGED ? rg.total_q : static_cast<cuuint64_t>(B) * T;
+  const cuuint64_t hd = HD, hq = Hq, hkv = Hkv;
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[3] = {hd, hq, rows}, strides[2] = {hd * 2, hq * hd * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tpt)};
+    if (!make_map_nd(&mq, q, 3, dims, strides, box)) return TTCD_ERR_CUDA;
+  }
+  SinkArgs a{};
+  if (PAGED) {
+    const cuuint64_t page = cuuint64_t(1) << pc.page_log2;
+    const cuuint64_t dims[2] = {hd, pc.n_pages * hkv * page}, strides[1] = {hd * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(page)};
+    if (!make_map_nd(&mk, pc.k, 2, dims, strides, box) ||
+        !make_map_nd(&mv, pc.v, 2, dims, strides, box))
+      return TTCD_ERR_CUDA;
+    a.rg = rg;
+    a.table = pc.table;
+    a.max_pages = pc.max_pages;
+    a.n_pages = pc.n_pages;
+    a.page_log2 = pc.page_log2;
+    a.oob_row = static_cast<int>(dims[1]);
+    a.n_units = static_cast<int>(tile_slots(rg.total_q, rg.n_seq, 2 * tpt));
+  } else {
+    const cuuint64_t dims[4] = {hd, hkv, static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
+    const cuuint64_t strides[3] = {hd * 2, hkv * hd * 2, hkv * hd * 2 * T};
+    const cuuint32_t box[4] = {64, 1, ATT_BN, 1};
+    if (!make_map_nd(&mk, k, 4, dims, strides, box) || !make_map_nd(&mv, v, 4, dims, strides, box))
+      return TTCD_ERR_CUDA;
+    a.n_units = cdiv(T, 2 * tpt);
+  }
+  a.o = static_cast<bf*>(o);
+  a.lse = lse;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = G;
+  a.tpt = tpt;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const long long items = static_cast<long long>(a.n_units) * Hkv * (PAGED ? 1 : B);
+  const long long keys = std::min<long long>(
+      static_cast<long long>(window) + 2 * tpt + n_sink,
+      PAGED ? static_cast<long long>(pc.max_pages) << pc.page_log2 : T);
+  a.splits = pick_splits(items, c.sms, (keys + ATT_BN - 1) / ATT_BN);
+  const long long grid = items * a.splits;
+  if (grid >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
+  auto kern = sink_window_attn_kernel<HD, PAGED>;
+  constexpr int smem = SinkCfg<HD>::SMEM;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return TTCD_ERR_CUDA;
+  TTCD_TRY(check_reg_split(reinterpret_cast<const void*>(kern), ATT_THREADS, kAttnRegSplit));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(ATT_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a, c.st) != cudaSuccess) {
+    cudaGetLastError();
+    return TTCD_ERR_CUDA;
+  }
   TTCD_CHECK_LAUNCH();
   return TTCD_OK;
 }
