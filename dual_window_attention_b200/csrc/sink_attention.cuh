@@ -55,96 +55,4 @@ __device__ __forceinline__ int seq_of_row(const Ragged& r, int row) {
   return last;
 }
 
-template <int HD>
-__device__ __forceinline__ void ld_lane(const __nv_bfloat16* row, int lane, float (&x)[HD / 32]) {
-#pragma unroll
-  for (int i = 0; i < HD / 32; ++i) x[i] = __bfloat162float(row[lane * (HD / 32) + i]);
-}
-template <int HD>
-__device__ __forceinline__ float warp_dot(const float (&a)[HD / 32], const float (&b)[HD / 32]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < HD / 32; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// Backward, one warp per (query row, head): dq.
-template <int HD>
-__global__ void sink_attn_dq_simple_kernel(const __nv_bfloat16* q, const __nv_bfloat16* k,
-                                           const __nv_bfloat16* v, const __nv_bfloat16* o,
-                                           const float* lse, const __nv_bfloat16* d_o,
-                                           __nv_bfloat16* dq, int B, int T, int Hq, int Hkv,
-                                           int window, int n_sink, float scale) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (item >= static_cast<long long>(B) * T * Hq) return;
-  const long long row = item / Hq;
-  const int h = static_cast<int>(item % Hq), g = h / (Hq / Hkv);
-  const int b = static_cast<int>(row / T), t = static_cast<int>(row % T);
-  float qf[E], of[E], gf[E], acc[E] = {};
-  ld_lane<HD>(q + item * HD, lane, qf);
-  ld_lane<HD>(o + item * HD, lane, of);
-  ld_lane<HD>(d_o + item * HD, lane, gf);
-  const float delta = warp_dot<HD>(of, gf);
-  const float ls = lse[(static_cast<long long>(b) * Hq + h) * T + t];
-  const KeyRange kr = key_range(t, t, window, n_sink);
-  for (int j = 0; j <= kr.hi; ++j) {
-    if (j == kr.sink_end && j < kr.lo) j = kr.lo;
-    const long long off = ((static_cast<long long>(b) * T + j) * Hkv + g) * HD;
-    float kf[E], vf[E];
-    ld_lane<HD>(k + off, lane, kf);
-    ld_lane<HD>(v + off, lane, vf);
-    const float p = __expf(warp_dot<HD>(qf, kf) * scale - ls);
-    const float ds = p * (warp_dot<HD>(gf, vf) - delta) * scale;
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = fmaf(ds, kf[i], acc[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i) dq[item * HD + lane * E + i] = __float2bfloat16_rn(acc[i]);
-}
-
-// Backward, one warp per (key row, KV head): dk and dv.
-template <int HD>
-__global__ void sink_attn_dkv_simple_kernel(const __nv_bfloat16* q, const __nv_bfloat16* k,
-                                            const __nv_bfloat16* v, const __nv_bfloat16* o,
-                                            const float* lse, const __nv_bfloat16* d_o,
-                                            __nv_bfloat16* dk, __nv_bfloat16* dv, int B, int T,
-                                            int Hq, int Hkv, int window, int n_sink, float scale) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (item >= static_cast<long long>(B) * T * Hkv) return;
-  const long long row = item / Hkv;
-  const int g = static_cast<int>(item % Hkv), G = Hq / Hkv;
-  const int b = static_cast<int>(row / T), j = static_cast<int>(row % T);
-  float kf[E], vf[E], ak[E] = {}, av[E] = {};
-  ld_lane<HD>(k + item * HD, lane, kf);
-  ld_lane<HD>(v + item * HD, lane, vf);
-  const int t_end = j < n_sink || window > T - j ? T : j + window;
-  for (int h = g * G; h < (g + 1) * G; ++h)
-    for (int t = j; t < t_end; ++t) {
-      const long long off = ((static_cast<long long>(b) * T + t) * Hq + h) * HD;
-      float qf[E], of[E], gf[E];
-      ld_lane<HD>(q + off, lane, qf);
-      ld_lane<HD>(o + off, lane, of);
-      ld_lane<HD>(d_o + off, lane, gf);
-      const float ls = lse[(static_cast<long long>(b) * Hq + h) * T + t];
-      const float p = __expf(warp_dot<HD>(qf, kf) * scale - ls);
-      const float ds = p * (warp_dot<HD>(gf, vf) - warp_dot<HD>(of, gf)) * scale;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        ak[i] = fmaf(ds, qf[i], ak[i]);
-        av[i] = fmaf(p, gf[i], av[i]);
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    dk[item * HD + lane * E + i] = __float2bfloat16_rn(ak[i]);
-    dv[item * HD + lane * E + i] = __float2bfloat16_rn(av[i]);
-  }
-}
-
 }  // namespace ttcd

@@ -1,0 +1,649 @@
+// Backward of the sliding-window attention with sinks on the tensor cores.
+//
+//   P = exp(scale Q K^T - lse),  dP = dO V^T,  dS = P (dP - delta),  delta_t = dO_t . O_t
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+//
+// Two kernels, each with its result in TMEM until it is stored once: dQ with the
+// queries standing, then dK and dV with the keys standing.  S and dP are formed in
+// both (7 products of a tile pair instead of 5), and in exchange nothing is added
+// into global memory: no fp32 dq buffer, no reductions through L2, and two
+// runs give the same bits.
+//
+// A tile of queries is floor(128 / G) tokens of the G heads of one KV head, as in
+// the forward, so a group of any size fills the 128 rows and shares K and V.
+//
+// Both kernels run 384 threads: warp 0 the TMA producer, warp 1 the MMA issuer
+// (one elected lane), warps 4..11 the element work on 128 x 128 scores, thread =
+// (TMEM lane, half of the columns).  p stays in registers in 32 bits between the
+// exponential and dS.  S and dP have one buffer each, and what alternates is the
+// work: while the element warps form P from S, the tensor cores run the products
+// of dS and the next dP, and while they form dS from dP the products of P and the
+// next S.
+//
+// dQ kernel.  Q and dO stand in TMEM as A operands (put there by the threads of
+// their rows, which also form delta), so that shared memory is read for K and V
+// alone: 128 x 128 x 16 steps with both operands in shared memory take all of its
+// 128 bytes per cycle.  Per key tile v: S(v+1), dQ(v) += dS K, dP(v+1), with dS
+// over its dP.  It also writes -log2(e) lse and -delta of its rows, packed as the
+// tiles are, for the second kernel.
+//
+// dK/dV kernel.  Per query tile v: dV += P^T dO, S^T(v+1) = K Q^T, dK += dS^T Q,
+// dP^T(v+1) = V dO^T; P^T lies over its S^T and dS^T over its dP^T as A operands.
+// The first key tile is seen by every query through its sinks: the query tiles
+// past its window are cut into items of their own, which write fp32 partial rows of the
+// sinks, and a last kernel adds them in a fixed order.
+#pragma once
+#include "attention_bwd.cuh"
+#include "sink_attention_fwd.cuh"
+
+namespace ttcd {
+
+struct SinkBwdArgs {
+  const __nv_bfloat16* q;    // [B, T, Hq, HD]
+  const __nv_bfloat16* o;
+  const __nv_bfloat16* d_o;
+  const float* lse;          // [B, Hq, T]
+  __nv_bfloat16* dq;         // [B, T, Hq, HD]
+  __nv_bfloat16* dk;         // [B, T, Hkv, HD]
+  __nv_bfloat16* dv;
+  float* rows;     // [B, Hkv, n_qt, 2, 128]: -log2(e) lse and -delta, packed rows
+  float* partial;  // [1 + n_far, B, Hkv, 2, n_sink, HD]: dk, dv of the sinks
+  int B, T, Hq, Hkv, G, tpt, n_qt, n_kt;
+  int window, n_sink;
+  int n_far, far_tiles;  // items of the far queries of the sinks, query tiles each
+  int far0;              // the first of these query tiles
+  float scale, scale_log2;
+};
+
+template <int HD>
+struct SinkDqCfg {
+  static constexpr int PANELS = HD / 64;
+  static constexpr int TILE = PANELS * 128 * 128;
+  static constexpr int KS = 3, VS = 3;
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = KS * TILE;
+  static constexpr int DEL_OFF = V_OFF + VS * TILE;  // 128 floats
+  static constexpr int BAR_OFF = DEL_OFF + 512;
+  static constexpr int SMEM_RAW = 1024 + BAR_OFF + 256;
+  // at least 120 KB: one CTA per SM (it takes all 512 TMEM columns)
+  static constexpr int SMEM = SMEM_RAW > 122880 ? SMEM_RAW : 122880;
+};
+
+template <int HD>
+struct SinkDkvCfg {
+  static constexpr int PANELS = HD / 64;
+  static constexpr int TILE = PANELS * 128 * 128;
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = TILE;
+  static constexpr int Q_OFF = 2 * TILE;   // two stages
+  static constexpr int DO_OFF = 4 * TILE;  // two stages
+  static constexpr int ROW_OFF = 6 * TILE;  // two stages of 2 x 128 floats
+  static constexpr int BAR_OFF = ROW_OFF + 2048;
+  static constexpr int SMEM_RAW = 1024 + BAR_OFF + 256;
+  static constexpr int SMEM = SMEM_RAW > 122880 ? SMEM_RAW : 122880;
+};
+
+// p = 2^(s scale_log2 + nl) of 64 scores; nl per pair of columns.  One pair in
+// four on the FMA pipe where `fine` (as the forward).
+template <bool FINE, class NL>
+__device__ __forceinline__ void probs64(float (&s)[64], float scale_log2, NL nl) {
+  const uint64_t sc2 = f2pack(scale_log2, scale_log2);
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    const uint64_t x = fma2(f2pack(s[c], s[c + 1]), sc2, nl(c));
+    if (FINE && ((c >> 1) & 3) == 3) {
+      f2unpack(exp2_poly2_fine(x), s[c], s[c + 1]);
+    } else {
+      float x0, x1;
+      f2unpack(x, x0, x1);
+      s[c] = ex2_approx(x0);
+      s[c + 1] = ex2_approx(x1);
+    }
+  }
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  float a, b;
+  f2unpack(x, a, b);
+  return pack_bf16x2(a, b);
+}
+// dS of 32 columns: p (dp + nd), packed bf16 pairs.
+template <class ND>
+__device__ __forceinline__ void ds32(const float* p, const float (&dp)[32], ND nd, uint32_t* out) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2)
+    out[i >> 1] = pack2(mul2(f2pack(p[i], p[i + 1]), add2(f2pack(dp[i], dp[i + 1]), nd(i))));
+}
+
+template <int HD>
+__global__ void __launch_bounds__(ATTB_THREADS, 1)
+    sink_attn_dq_kernel(const __grid_constant__ CUtensorMap mapK,
+                        const __grid_constant__ CUtensorMap mapV, const SinkBwdArgs a,
+                        const DevStatus st) {
+  using Cfg = SinkDqCfg<HD>;
+  constexpr int KS = Cfg::KS, VS = Cfg::VS, PANEL = 128 * 128;
+  constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);  // S, dP
+  constexpr uint32_t ID_DQ = idesc_bf16_f32(128, HD, false, true);
+  constexpr uint32_t C_S = 0, C_DP = 128, C_DQ = 256, C_Q = 384, C_DO = 448;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF);
+  uint64_t* k_full = bars;             // KS
+  uint64_t* k_empty = k_full + KS;     // KS
+  uint64_t* v_full = k_empty + KS;     // VS
+  uint64_t* v_empty = v_full + VS;     // VS
+  uint64_t* a_ready = v_empty + VS;    // Q and dO are in TMEM (256 arrivals)
+  uint64_t* s_full = a_ready + 1;
+  uint64_t* s_free = s_full + 1;       // 256 arrivals
+  uint64_t* dp_full = s_free + 1;
+  uint64_t* ds_ready = dp_full + 1;    // 256 arrivals
+  uint64_t* done = ds_ready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* del = reinterpret_cast<float*>(smem + Cfg::DEL_OFF);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int hk = static_cast<int>(blockIdx.x) % a.Hkv;
+  const int b = static_cast<int>(blockIdx.x) / a.Hkv % a.B;
+  // longest (latest) tiles first
+  const int qt = a.n_qt - 1 - static_cast<int>(blockIdx.x) / (a.Hkv * a.B);
+  const int t0 = qt * a.tpt, t1 = min(t0 + a.tpt, a.T) - 1;
+  const KeyRange kr = key_range(t0, t1, a.window, a.n_sink);
+  const int jhi = kr.hi / 128, n_win = jhi - kr.lo / 128 + 1;
+  const int nv = n_win + (kr.sink_end > 0 && kr.lo >= 128 ? 1 : 0);
+  auto key_tile = [&](int v) { return v < n_win ? jhi - v : 0; };
+
+  if (threadIdx.x == 0) {
+    for (uint64_t* p = bars; p <= done; ++p)
+      mbar_init(p, p == a_ready || p == s_free || p == ds_ready ? 256 : 1);
+    *abort = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&mapK);
+    tma_prefetch_map(&mapV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // 128 x 56 + 256 x 224 = 384 x 168 registers
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------- TMA producer
+      int issued_k = 0, issued_v = 0;
+      auto load = [&](int off, const CUtensorMap* map, uint64_t* bar, int v) {
+        mbar_arrive_expect_tx(bar, Cfg::TILE);
+#pragma unroll
+        for (int p = 0; p < Cfg::PANELS; ++p)
+          tma_load_4d(smem + off + p * PANEL, map, bar, 64 * p, hk, key_tile(v) * 128, b);
+      };
+      for (int v = 0; v < nv; ++v) {
+        const int ks = v % KS, vs = v % VS;
+        if (!mbar_wait(&k_empty[ks], ((v / KS) & 1) ^ 1, st, abort)) break;
+        load(Cfg::K_OFF + ks * Cfg::TILE, &mapK, &k_full[ks], v);
+        ++issued_k;
+        if (!mbar_wait(&v_empty[vs], ((v / VS) & 1) ^ 1, st, abort)) break;
+        load(Cfg::V_OFF + vs * Cfg::TILE, &mapV, &v_full[vs], v);
+        ++issued_v;
+      }
+      // every load issued lands before the CTA can exit
+      volatile int no_abort = 0;
+      for (int j = max(0, issued_k - KS); j < issued_k; ++j)
+        mbar_wait(&k_full[j % KS], (j / KS) & 1, st, &no_abort);
+      for (int j = max(0, issued_v - VS); j < issued_v; ++j)
+        mbar_wait(&v_full[j % VS], (j / VS) & 1, st, &no_abort);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------- MMA issuer
+      constexpr uint32_t HI = sdesc_hi_sw128(1024);
+      const uint32_t k_lo = sdesc_lo(smem_u32(smem + Cfg::K_OFF), 16);
+      const uint32_t v_lo = sdesc_lo(smem_u32(smem + Cfg::V_OFF), 16);
+      const uint32_t k_mn = sdesc_lo(smem_u32(smem + Cfg::K_OFF), PANEL);
+      auto koff = [](int kk) { return static_cast<uint32_t>(((kk >> 2) * PANEL + (kk & 3) * 32) >> 4); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, st, abort));
+        tc_fence_after();
+        return ok;
+      };
+      auto issue_s = [&](int v) {  // S = Q K^T
+        const uint32_t kb = k_lo + (((v % KS) * Cfg::TILE) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_bf16_ts_lh(tmem + C_S, tmem + C_Q + kk * 8, kb + koff(kk), HI, ID_S, kk > 0 ? 1u : 0u);
+          mma_commit(s_full);
+        }
+        __syncwarp();
+      };
+      auto issue_dp = [&](int v) {  // dP = dO V^T
+        const uint32_t vb = v_lo + (((v % VS) * Cfg::TILE) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_bf16_ts_lh(tmem + C_DP, tmem + C_DO + kk * 8, vb + koff(kk), HI, ID_S, kk > 0 ? 1u : 0u);
+          mma_commit(dp_full);
+          mma_commit(&v_empty[v % VS]);
+        }
+        __syncwarp();
+      };
+      bool ok = wait(a_ready, 0) && wait(&k_full[0], 0);
+      if (ok) {
+        issue_s(0);
+        ok = wait(&v_full[0], 0);
+        if (ok) issue_dp(0);
+      }
+      for (int v = 0; v < nv && ok; ++v) {
+        const bool more = v + 1 < nv;
+        if (more) {
+          if (!wait(s_free, v & 1) || !wait(&k_full[(v + 1) % KS], ((v + 1) / KS) & 1)) break;
+          issue_s(v + 1);
+        }
+        if (!wait(ds_ready, v & 1)) break;
+        const uint32_t kb = k_mn + (((v % KS) * Cfg::TILE) >> 4);
+        if (elect_one()) {  // dQ += dS K; the halves of dS over the halves of dP
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts_lh(tmem + C_DQ, tmem + C_DP + (kk >> 2) * 64 + (kk & 3) * 8,
+                           kb + ((kk * 2048) >> 4), HI, ID_DQ, (v > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&k_empty[v % KS]);
+        }
+        __syncwarp();
+        if (more) {
+          if (!wait(&v_full[(v + 1) % VS], ((v + 1) / VS) & 1)) break;
+          issue_dp(v + 1);
+        }
+      }
+      if (elect_one()) mma_commit(done);
+      __syncwarp();
+      volatile int no_abort = 0;
+      mbar_wait(done, 0, st, &no_abort);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+    // --------------------------------------------------------------- query rows
+    const int h = (warp - 4) >> 2;  // half of the columns
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const int tok = r / a.G, head = hk * a.G + r % a.G;
+    const int t = t0 + tok;
+    const bool row_ok = tok < a.tpt && t < a.T;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const long long row = (static_cast<long long>(b) * a.T + t) * a.Hq + head;
+    float* rows = a.rows + ((static_cast<long long>(b) * a.Hkv + hk) * a.n_qt + qt) * 256;
+    float nl = 0.f;
+    if (row_ok) nl = -a.lse[(static_cast<long long>(b) * a.Hq + head) * a.T + t] * 1.4426950408889634f;
+    {  // this row of Q (first half) or dO (second half) into TMEM; rows that are not there: zeros
+      uint32_t w[HD / 2];
+      const uint4* src = reinterpret_cast<const uint4*>((h ? a.d_o : a.q) + row * HD);
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) {
+        const uint4 x = row_ok ? src[i] : make_uint4(0, 0, 0, 0);
+        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int c = 0; c < HD / 2; c += 32)
+        tmem_st32(tmem + lane_off + (h ? C_DO : C_Q) + c, *reinterpret_cast<uint32_t(*)[32]>(&w[c]));
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(a_ready);
+      if (h) {
+        const uint4* os = reinterpret_cast<const uint4*>(a.o + row * HD);
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) {
+          const uint4 x = row_ok ? os[i] : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            d = fmaf(bf16lo_to_f32(u[e]), bf16lo_to_f32(w[4 * i + e]), d);
+            d = fmaf(bf16hi_to_f32(u[e]), bf16hi_to_f32(w[4 * i + e]), d);
+          }
+        }
+        del[r] = -d;
+        rows[128 + r] = -d;
+      } else {
+        rows[r] = row_ok ? nl : -INFINITY;
+      }
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const uint64_t nd2 = f2pack(del[r], del[r]), nl2 = f2pack(nl, nl);
+    const uint32_t s_addr = tmem + lane_off + C_S + 64 * h, dp_addr = tmem + lane_off + C_DP + 64 * h;
+    bool ok = true;
+    for (int v = 0; v < nv; ++v) {
+      const int k0 = key_tile(v) * 128;
+      if (!mbar_wait(s_full, v & 1, st, abort)) { ok = false; break; }
+      tc_fence_after();
+      float p[64];
+      tmem_ld_cols<64>(s_addr, p);
+      tc_fence_before();
+      mbar_arrive(s_free);
+      const bool unmasked =
+          k0 + 127 <= t0 && (k0 > t1 - a.window || k0 + 128 <= a.n_sink);
+      if (unmasked) {
+        probs64<true>(p, a.scale_log2, [&](int) { return nl2; });
+      } else {
+        const int c0 = k0 + 64 * h;
+        const int hi = t - c0, lo = t - a.window + 1 - c0, ns = a.n_sink - c0;
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          p[c] = (c <= hi && (c >= lo || c < ns)) ? p[c] : -INFINITY;
+        probs64<false>(p, a.scale_log2, [&](int) { return nl2; });
+      }
+      if (!mbar_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t D[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        float dp[32];
+        tmem_ld32f(dp_addr + c, dp);
+        ds32(&p[c], dp, [&](int) { return nd2; }, &D[c >> 1]);
+      }
+      tmem_st32(dp_addr, D);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(ds_ready);
+    }
+    if (ok && mbar_wait(done, 0, st, abort)) {
+      tc_fence_after();
+      // half of the row's columns each
+      __nv_bfloat16* dst = a.dq + row * HD + h * (HD / 2);
+#pragma unroll
+      for (int c = 0; c < HD / 2; c += 32) {
+        float x[32];
+        tmem_ld32f(tmem + lane_off + C_DQ + h * (HD / 2) + c, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] *= a.scale;
+        if (row_ok) store_x32(dst + c, x);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(ATTB_THREADS, 1)
+    sink_attn_dkv_kernel(const __grid_constant__ CUtensorMap mapQ,
+                         const __grid_constant__ CUtensorMap mapK,
+                         const __grid_constant__ CUtensorMap mapV,
+                         const __grid_constant__ CUtensorMap mapDO, const SinkBwdArgs a,
+                         const DevStatus st) {
+  using Cfg = SinkDkvCfg<HD>;
+  constexpr int PANEL = 128 * 128;
+  constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);  // S^T, dP^T
+  constexpr uint32_t ID_KV = idesc_bf16_f32(128, HD, false, true);   // dK, dV
+  constexpr uint32_t C_S = 0, C_DP = 128, C_DK = 256, C_DV = 384;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF);
+  uint64_t* kv_full = bars;
+  uint64_t* q_full = bars + 1;    // 2 (Q and the rows' lse, delta)
+  uint64_t* q_empty = bars + 3;   // 2
+  uint64_t* do_full = bars + 5;   // 2
+  uint64_t* do_empty = bars + 7;  // 2
+  uint64_t* s_full = bars + 9;
+  uint64_t* p_ready = bars + 10;  // 256 arrivals
+  uint64_t* dp_full = bars + 11;
+  uint64_t* ds_ready = bars + 12; // 256 arrivals
+  uint64_t* done = bars + 13;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int hk = static_cast<int>(blockIdx.x) % a.Hkv;
+  const int b = static_cast<int>(blockIdx.x) / a.Hkv % a.B;
+  const int item = static_cast<int>(blockIdx.x) / (a.Hkv * a.B);
+  const bool far = item < a.n_far;
+  const int kt = far ? 0 : item - a.n_far;
+  const int k0 = kt * 128;
+  // query tiles [qt0, qt0 + nv)
+  const int qt0 = far ? a.far0 + item * a.far_tiles : k0 / a.tpt;
+  const int nv = (far ? min(qt0 + a.far_tiles, a.n_qt)
+                      : min(a.T - 1, k0 + 127 + a.window - 1) / a.tpt + 1) - qt0;
+  const int rows_used = a.G * a.tpt;
+
+  if (threadIdx.x == 0) {
+    for (uint64_t* p = bars; p <= done; ++p) mbar_init(p, p == p_ready || p == ds_ready ? 256 : 1);
+    *abort = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&mapQ);
+    tma_prefetch_map(&mapK);
+    tma_prefetch_map(&mapV);
+    tma_prefetch_map(&mapDO);
+  }
+  // rows of the Q and dO stages that no load writes: zeros (their P is 0, and 0
+  // times what lies there must be 0)
+  for (int i = threadIdx.x; i < (128 - rows_used) * 8 * Cfg::PANELS * 4; i += ATTB_THREADS) {
+    const int c = i & 7, x = i >> 3, panel = x % (Cfg::PANELS * 4), r = rows_used + x / (Cfg::PANELS * 4);
+    *reinterpret_cast<uint4*>(smem + Cfg::Q_OFF + panel * PANEL + r * 128 + c * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+  fence_async_smem();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------- TMA producer
+      const uint32_t bytes = Cfg::PANELS * 128 * rows_used;
+      const float* rows = a.rows + (static_cast<long long>(b) * a.Hkv + hk) * a.n_qt * 256;
+      mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE);
+#pragma unroll
+      for (int p = 0; p < Cfg::PANELS; ++p) {
+        tma_load_4d(smem + Cfg::K_OFF + p * PANEL, &mapK, kv_full, 64 * p, hk, k0, b);
+        tma_load_4d(smem + Cfg::V_OFF + p * PANEL, &mapV, kv_full, 64 * p, hk, k0, b);
+      }
+      int issued_q = 0, issued_do = 0;
+      for (int v = 0; v < nv; ++v) {
+        const int sg = v & 1, qt = qt0 + v;
+        const uint32_t ph = ((v >> 1) & 1) ^ 1;
+        if (!mbar_wait(&q_empty[sg], ph, st, abort)) break;
+        mbar_arrive_expect_tx(&q_full[sg], bytes + 1024);
+#pragma unroll
+        for (int p = 0; p < Cfg::PANELS; ++p)
+          tma_load_4d(smem + Cfg::Q_OFF + sg * Cfg::TILE + p * PANEL, &mapQ, &q_full[sg], 64 * p,
+                      hk * a.G, qt * a.tpt, b);
+        bulk_load(smem + Cfg::ROW_OFF + sg * 1024, rows + qt * 256ll, 1024, &q_full[sg]);
+        ++issued_q;
+        if (!mbar_wait(&do_empty[sg], ph, st, abort)) break;
+        mbar_arrive_expect_tx(&do_full[sg], bytes);
+#pragma unroll
+        for (int p = 0; p < Cfg::PANELS; ++p)
+          tma_load_4d(smem + Cfg::DO_OFF + sg * Cfg::TILE + p * PANEL, &mapDO, &do_full[sg], 64 * p,
+                      hk * a.G, qt * a.tpt, b);
+        ++issued_do;
+      }
+      volatile int no_abort = 0;
+      mbar_wait(kv_full, 0, st, &no_abort);
+      for (int j = max(0, issued_q - 2); j < issued_q; ++j)
+        mbar_wait(&q_full[j & 1], (j >> 1) & 1, st, &no_abort);
+      for (int j = max(0, issued_do - 2); j < issued_do; ++j)
+        mbar_wait(&do_full[j & 1], (j >> 1) & 1, st, &no_abort);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------- MMA issuer
+      constexpr uint32_t HI = sdesc_hi_sw128(1024);
+      constexpr uint32_t STAGE = Cfg::TILE >> 4;
+      const uint32_t k_lo = sdesc_lo(smem_u32(smem + Cfg::K_OFF), 16);
+      const uint32_t v_lo = sdesc_lo(smem_u32(smem + Cfg::V_OFF), 16);
+      const uint32_t q_lo = sdesc_lo(smem_u32(smem + Cfg::Q_OFF), 16);
+      const uint32_t do_lo = sdesc_lo(smem_u32(smem + Cfg::DO_OFF), 16);
+      const uint32_t q_mn = sdesc_lo(smem_u32(smem + Cfg::Q_OFF), PANEL);
+      const uint32_t do_mn = sdesc_lo(smem_u32(smem + Cfg::DO_OFF), PANEL);
+      auto koff = [](int kk) { return static_cast<uint32_t>(((kk >> 2) * PANEL + (kk & 3) * 32) >> 4); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, st, abort));
+        tc_fence_after();
+        return ok;
+      };
+      auto issue_scores = [&](uint32_t d, uint32_t a_lo, uint32_t b_lo, uint64_t* bar) {
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            mma_bf16_ss_lh(tmem + d, a_lo + koff(kk), HI, b_lo + koff(kk), HI, ID_S, kk > 0 ? 1u : 0u);
+          mma_commit(bar);
+        }
+        __syncwarp();
+      };
+      // += P^T dO or dS^T Q; the halves of the A operand over the halves of its scores
+      auto issue_acc = [&](uint32_t d, uint32_t at, uint32_t b_mn, bool first, uint64_t* bar) {
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts_lh(tmem + d, tmem + at + (kk >> 2) * 64 + (kk & 3) * 8,
+                           b_mn + ((kk * 2048) >> 4), HI, ID_KV, (!first || kk > 0) ? 1u : 0u);
+          mma_commit(bar);
+        }
+        __syncwarp();
+      };
+      bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
+      if (ok) {
+        issue_scores(C_S, k_lo, q_lo, s_full);
+        ok = wait(&do_full[0], 0);
+        if (ok) issue_scores(C_DP, v_lo, do_lo, dp_full);
+      }
+      for (int v = 0; v < nv && ok; ++v) {
+        const uint32_t sg = v & 1, nx = sg ^ 1, nph = ((v + 1) >> 1) & 1;
+        const bool more = v + 1 < nv;
+        if (!wait(p_ready, v & 1)) break;
+        issue_acc(C_DV, C_S, do_mn + sg * STAGE, v == 0, &do_empty[sg]);
+        if (more) {
+          if (!wait(&q_full[nx], nph)) break;
+          issue_scores(C_S, k_lo, q_lo + nx * STAGE, s_full);
+        }
+        if (!wait(ds_ready, v & 1)) break;
+        issue_acc(C_DK, C_DP, q_mn + sg * STAGE, v == 0, &q_empty[sg]);
+        if (more) {
+          if (!wait(&do_full[nx], nph)) break;
+          issue_scores(C_DP, v_lo, do_lo + nx * STAGE, dp_full);
+        }
+      }
+      if (elect_one()) mma_commit(done);
+      __syncwarp();
+      volatile int no_abort = 0;
+      mbar_wait(done, 0, st, &no_abort);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+    // ----------------------------------------------------------------- key rows
+    const int h = (warp - 4) >> 2;  // half of the columns
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const int j = k0 + r;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + C_S + 64 * h, dp_addr = tmem + lane_off + C_DP + 64 * h;
+    bool ok = true;
+    for (int v = 0; v < nv; ++v) {
+      const int t0 = (qt0 + v) * a.tpt, t1 = t0 + a.tpt - 1;
+      if (!mbar_wait(&q_full[v & 1], (v >> 1) & 1, st, abort)) { ok = false; break; }
+      const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + Cfg::ROW_OFF + (v & 1) * 1024 + h * 256);
+      const ulonglong2* nd = nl + 32;
+      if (!mbar_wait(s_full, v & 1, st, abort)) { ok = false; break; }
+      tc_fence_after();
+      float p[64];
+      tmem_ld_cols<64>(s_addr, p);
+      auto pair = [](const ulonglong2* x, int c) { return (c & 2) ? x[c >> 2].y : x[c >> 2].x; };
+      const bool unmasked =
+          k0 + 127 <= t0 && (t1 - a.window < k0 || k0 + 128 <= a.n_sink);
+      if (unmasked) {
+        probs64<true>(p, a.scale_log2, [&](int c) { return pair(nl, c); });
+      } else {
+        // columns (token, head) of the tokens from j to the last that sees it
+        const int lo = max(j - t0, 0) * a.G - 64 * h;
+        const int last = j < a.n_sink ? 128 : min(max(j + a.window - t0, 0), 128);
+        const int hi = last * a.G - 64 * h;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c < hi) ? p[c] : -INFINITY;
+        probs64<false>(p, a.scale_log2, [&](int c) { return pair(nl, c); });
+      }
+      uint32_t P[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) P[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
+      tmem_st32(s_addr, P);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(p_ready);
+      if (!mbar_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        float dp[32];
+        tmem_ld32f(dp_addr + c, dp);
+        ds32(&p[c], dp, [&](int i) { return pair(nd, c + i); }, &P[c >> 1]);
+      }
+      tmem_st32(dp_addr, P);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(ds_ready);
+    }
+    // ------------------------------------------------- dK (first half), dV rows
+    if (ok && mbar_wait(done, 0, st, abort)) {
+      tc_fence_after();
+      const float f = h ? 1.f : a.scale;
+      const bool part = a.n_far > 0 && kt == 0 && r < a.n_sink;  // a sum of several items
+      const long long bh = static_cast<long long>(b) * a.Hkv + hk;
+      float* ps = a.partial +
+          ((((far ? item + 1 : 0) * static_cast<long long>(a.B) * a.Hkv + bh) * 2 + h) * a.n_sink + r) * HD;
+      __nv_bfloat16* dst = (h ? a.dv : a.dk) + ((static_cast<long long>(b) * a.T + j) * a.Hkv + hk) * HD;
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        float x[32];
+        tmem_ld32f(tmem + lane_off + (h ? C_DV : C_DK) + c, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] *= f;
+        if (part && j < a.T)
+          store_f32x32(ps + c, x);
+        else if (!far && j < a.T)
+          store_x32(dst + c, x);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dk and dv of the sinks: the sum of the partial rows, in the items' order.
+// One thread per element; T > n_sink wherever there are far items.
+template <int HD>
+__global__ void sink_attn_join_kernel(const SinkBwdArgs a) {
+  const long long per = static_cast<long long>(a.B) * a.Hkv * 2 * a.n_sink * HD;
+  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= per) return;
+  float x = 0.f;
+  for (int f = 0; f <= a.n_far; ++f) x += a.partial[f * per + i];
+  const int c = static_cast<int>(i % HD);
+  long long y = i / HD;
+  const int r = static_cast<int>(y % a.n_sink);
+  y /= a.n_sink;
+  const int which = static_cast<int>(y & 1);
+  y >>= 1;
+  const int hk = static_cast<int>(y % a.Hkv);
+  const long long b = y / a.Hkv;
+  (which ? a.dv : a.dk)[((b * a.T + r) * a.Hkv + hk) * HD + c] = __float2bfloat16_rn(x);
+}
+
+}  // namespace ttcd

@@ -24,6 +24,7 @@
 #include "attention_bwd.cuh"
 #include "sink_attention.cuh"
 #include "sink_attention_fwd.cuh"
+#include "sink_attention_bwd.cuh"
 #include "paged_append.cuh"
 
 using namespace ttcd;
@@ -2789,30 +2790,100 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   return TTCD_OK;
 }
 
+// The backward's items: query tiles, key tiles, and the query tiles past the
+// window of the first key tile (far0 ...), cut into items of `far_tiles`: about as
+// long as the others (the query tiles of one window), at least 16 query tiles so
+// that an item is worth its prologue, and at most 64 partial sums.
+struct SinkBwdPlan {
+  int tpt, n_qt, n_kt, far0, far_tiles, n_far;
+  size_t rows_off, partial_off, bytes;
+};
+SinkBwdPlan plan_sink_bwd(int B, int T, int Hq, int Hkv, int hd, int window, int n_sink) {
+  SinkBwdPlan p{};
+  p.tpt = ATT_BM / (Hq / Hkv);
+  p.n_qt = cdiv(T, p.tpt);
+  p.n_kt = cdiv(T, 128);
+  p.far0 = std::min(T - 1, window + 126) / p.tpt + 1;
+  const int far = n_sink > 0 ? p.n_qt - p.far0 : 0;
+  if (far > 0) {
+    p.far_tiles = std::max({16, cdiv(std::min(window + 127, T), p.tpt), cdiv(far, 64)});
+    p.n_far = cdiv(far, p.far_tiles);
+  }
+  const size_t heads = static_cast<size_t>(B) * Hkv;
+  p.rows_off = kStatusBytes;
+  p.partial_off = p.rows_off + heads * p.n_qt * 256 * sizeof(float);
+  p.bytes = p.partial_off;
+  if (p.n_far > 0)
+    p.bytes += (1 + static_cast<size_t>(p.n_far)) * heads * 2 * n_sink * hd * sizeof(float);
+  return p;
+}
+
 template <int HD>
 ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const void* v,
                             const void* o, const float* lse, const void* d_o, void* dq, void* dk,
                             void* dv, int B, int T, int Hq, int Hkv, int window, int n_sink,
-                            float scale) {
+                            float scale, void* ws) {
   using bf = __nv_bfloat16;
-  const bf *q_ = static_cast<const bf*>(q), *k_ = static_cast<const bf*>(k),
-           *v_ = static_cast<const bf*>(v), *o_ = static_cast<const bf*>(o),
-           *g_ = static_cast<const bf*>(d_o);
-  const long long BT = static_cast<long long>(B) * T;
-  sink_attn_dq_simple_kernel<HD><<<static_cast<unsigned>(cdiv(BT * Hq, 8)), 256, 0, c.s>>>(
-      q_, k_, v_, o_, lse, g_, static_cast<bf*>(dq), B, T, Hq, Hkv, window, n_sink, scale);
+  const SinkBwdPlan p = plan_sink_bwd(B, T, Hq, Hkv, HD, window, n_sink);
+  SinkBwdArgs a{};
+  a.q = static_cast<const bf*>(q);
+  a.o = static_cast<const bf*>(o);
+  a.d_o = static_cast<const bf*>(d_o);
+  a.lse = lse;
+  a.dq = static_cast<bf*>(dq);
+  a.dk = static_cast<bf*>(dk);
+  a.dv = static_cast<bf*>(dv);
+  a.rows = reinterpret_cast<float*>(static_cast<char*>(ws) + p.rows_off);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.partial_off);
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.tpt = p.tpt;
+  a.n_qt = p.n_qt;
+  a.n_kt = p.n_kt;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.n_far = p.n_far;
+  a.far_tiles = p.far_tiles;
+  a.far0 = p.far0;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const long long heads = static_cast<long long>(B) * Hkv;
+  const long long grid_q = heads * p.n_qt, grid_k = heads * (p.n_far + p.n_kt);
+  if (grid_q >= (1ll << 31) || grid_k >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
+  CUtensorMap mq, mk, mv, mdo;
+  const cuuint64_t hd = HD, hq = Hq, hkv = Hkv, t = T;
+  const cuuint64_t qd[4] = {hd, hq, t, static_cast<cuuint64_t>(B)};
+  const cuuint64_t qs[3] = {hd * 2, hq * hd * 2, hq * hd * 2 * t};
+  const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(a.tpt), 1};
+  const cuuint64_t kd[4] = {hd, hkv, t, static_cast<cuuint64_t>(B)};
+  const cuuint64_t ks[3] = {hd * 2, hkv * hd * 2, hkv * hd * 2 * t};
+  const cuuint32_t kb[4] = {64, 1, 128, 1};
+  if (!make_map_nd(&mq, q, 4, qd, qs, qb) || !make_map_nd(&mdo, d_o, 4, qd, qs, qb) ||
+      !make_map_nd(&mk, k, 4, kd, ks, kb) || !make_map_nd(&mv, v, 4, kd, ks, kb))
+    return TTCD_ERR_CUDA;
+  auto kq = sink_attn_dq_kernel<HD>;
+  auto kk = sink_attn_dkv_kernel<HD>;
+  constexpr int smem_q = SinkDqCfg<HD>::SMEM, smem_k = SinkDkvCfg<HD>::SMEM;
+  if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q) != cudaSuccess ||
+      cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_k) != cudaSuccess)
+    return TTCD_ERR_CUDA;
+  TTCD_TRY(check_reg_split(reinterpret_cast<const void*>(kq), ATTB_THREADS, kAttnRegSplit));
+  TTCD_TRY(check_reg_split(reinterpret_cast<const void*>(kk), ATTB_THREADS, kAttnRegSplit));
+  kq<<<static_cast<unsigned>(grid_q), ATTB_THREADS, smem_q, c.s>>>(mk, mv, a, c.st);
   TTCD_CHECK_LAUNCH();
-  sink_attn_dkv_simple_kernel<HD><<<static_cast<unsigned>(cdiv(BT * Hkv, 8)), 256, 0, c.s>>>(
-      q_, k_, v_, o_, lse, g_, static_cast<bf*>(dk), static_cast<bf*>(dv), B, T, Hq, Hkv, window,
-      n_sink, scale);
+  kk<<<static_cast<unsigned>(grid_k), ATTB_THREADS, smem_k, c.s>>>(mq, mk, mv, mdo, a, c.st);
   TTCD_CHECK_LAUNCH();
+  if (p.n_far > 0) {
+    const long long n = heads * 2 * n_sink * HD;
+    sink_attn_join_kernel<HD><<<static_cast<unsigned>((n + 255) / 256), 256, 0, c.s>>>(a);
+    TTCD_CHECK_LAUNCH();
+  }
   return TTCD_OK;
 }
 
-size_t sink_bwd_ws_bytes(int B, int T, int Hq, int Hkv, int hd, int window, int n_sink) {
-  (void)B; (void)T; (void)Hq; (void)Hkv; (void)hd; (void)window; (void)n_sink;
-  return kStatusBytes;
-}
 ttcd_status check_sink_bwd(int B, int T, int Hq, int Hkv, int hd, int window, int n_sink) {
   if (B < 1 || T < 1) return TTCD_ERR_INVALID_ARG;
   TTCD_TRY(check_sink_shape(Hq, Hkv, hd, window, n_sink, 0.f, TTCD_BF16));
@@ -2852,7 +2923,7 @@ ttcd_status ttcd_sink_window_attn(const void* q, const void* k, const void* v, v
 size_t ttcd_sink_window_attn_backward_workspace_size(int B, int T, int Hq, int Hkv, int hd,
                                                      int window, int n_sink) {
   if (check_sink_bwd(B, T, Hq, Hkv, hd, window, n_sink) != TTCD_OK) return 0;
-  return sink_bwd_ws_bytes(B, T, Hq, Hkv, hd, clamp_window(window), n_sink);
+  return plan_sink_bwd(B, T, Hq, Hkv, hd, clamp_window(window), n_sink).bytes;
 }
 
 ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const void* v,
@@ -2866,13 +2937,13 @@ ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const v
   for (const void* x : need)
     if (!aligned16(x)) return TTCD_ERR_INVALID_ARG;
   const int w = clamp_window(window);
-  if (ws_bytes < sink_bwd_ws_bytes(B, T, Hq, Hkv, hd, w, n_sink)) return TTCD_ERR_WORKSPACE;
+  if (ws_bytes < plan_sink_bwd(B, T, Hq, Hkv, hd, w, n_sink).bytes) return TTCD_ERR_WORKSPACE;
   Ctx c;
   TTCD_TRY(make_ctx(stream, c, workspace));
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(hd));
   if (hd == 64)
-    return launch_sink_bwd<64>(c, q, k, v, o, lse, d_o, dq, dk, dv, B, T, Hq, Hkv, w, n_sink, sc);
-  return launch_sink_bwd<128>(c, q, k, v, o, lse, d_o, dq, dk, dv, B, T, Hq, Hkv, w, n_sink, sc);
+    return launch_sink_bwd<64>(c, q, k, v, o, lse, d_o, dq, dk, dv, B, T, Hq, Hkv, w, n_sink, sc, workspace);
+  return launch_sink_bwd<128>(c, q, k, v, o, lse, d_o, dq, dk, dv, B, T, Hq, Hkv, w, n_sink, sc, workspace);
 }
 
 ttcd_status ttcd_paged_kv_append(const void* qkv, void* q_out, void* k_pages, void* v_pages,
