@@ -50,6 +50,18 @@ TTCD_HD long long tile_slots(int total_q, int n_seq, int tpt) {
   return static_cast<long long>(total_q / tpt) + n_seq;
 }
 
+// Units of tpt tokens, another numbering: the first unit of sequence s has slot s,
+// and its unit i >= 1 slot n_seq + extra_slot(q_start[s]) + i - 1.  These do not
+// meet either, because floor((a + n) / tpt) >= floor(a / tpt) + ceil(n / tpt) - 1,
+// and lie below n_seq + total_q / tpt; such a slot belongs to the last sequence
+// whose first one is not beyond it (and to none if that has fewer units).
+TTCD_HD int extra_slot(int q_start, int tpt) { return q_start / tpt; }
+// First token of the unit at extra slot x of a sequence that begins at q_start.
+TTCD_HD int extra_token(int x, int q_start, int tpt) {
+  const long long t = (static_cast<long long>(x) - extra_slot(q_start, tpt) + 1) * tpt;
+  return t < (1 << 30) ? static_cast<int>(t) : (1 << 30);
+}
+
 // Keys that a tile with the positions [t_lo, t_hi] sees: [lo, t_hi] and the
 // sinks [0, sink_end) before lo.
 struct KeyRange {

@@ -41,6 +41,20 @@ __device__ __forceinline__ int find_seq(const Ragged& r, long long slot, int tpt
   return last;
 }
 
+// Sequence of a slot of the further units (those after a sequence's first): the
+// last one whose first such slot is not beyond it.
+__device__ __forceinline__ int find_extra_seq(const Ragged& r, int slot, int tpt) {
+  const int lane = threadIdx.x & 31;
+  int last = -1;
+  for (int s0 = 0; s0 < r.n_seq; s0 += 32) {
+    const int s = s0 + lane;
+    const unsigned m = __ballot_sync(0xffffffffu, s < r.n_seq && extra_slot(r.q_start[s], tpt) <= slot);
+    if (m) last = s0 + 31 - __clz(m);
+    if (m != 0xffffffffu) break;
+  }
+  return last;
+}
+
 // Sequence of a row of the packed queries: the last one that begins at or before
 // it (one warp, every lane gets the answer; -1: none).
 __device__ __forceinline__ int seq_of_row(const Ragged& r, int row) {

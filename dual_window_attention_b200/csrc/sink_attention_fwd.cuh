@@ -52,6 +52,7 @@ struct SinkArgs {
   int window, n_sink;
   float scale_log2;
   int splits;        // CTAs per cluster
+  int min_q;         // paged: sequences with fewer new tokens are another kernel's
 };
 
 template <int HD>
@@ -175,6 +176,9 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* unit = reinterpret_cast<int*>(tmem_slot + 2);  // paged: sequence, first token, span
 
+  // the kernel of the short sequences may start beside the last of these CTAs
+  if (PAGED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = a.splits > 1 ? static_cast<int>(blockIdx.x) % a.splits : 0;
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       if (s >= 0) {
         sp = load_span(a.rg, s, capacity);
         const long long t0 = (slot - tile_slot(sp.q0, s, tpu)) * tpu;
-        if (t0 >= sp.n) sp.n = 0;
+        if (t0 >= sp.n || sp.n < a.min_q) sp.n = 0;
         tok = static_cast<int>(t0);
       }
       if (lane == 0) {

@@ -25,6 +25,7 @@
 #include "sink_attention.cuh"
 #include "sink_attention_fwd.cuh"
 #include "sink_attention_bwd.cuh"
+#include "paged_decode.cuh"
 #include "paged_append.cuh"
 
 using namespace ttcd;
@@ -154,6 +155,30 @@ ttcd_status check_reg_split(const void* kern, int threads, const RegSplit& s) {
   const long long need = static_cast<long long>(s.threads_low) * s.regs_low +
                          static_cast<long long>(s.threads_high) * s.regs_high;
   return need <= pool ? TTCD_OK : TTCD_ERR_UNSUPPORTED;
+}
+
+// The attributes that KERN is launched with, set and checked at its first launch
+// on a device (0.5 us each, of a call's 5): its dynamic shared memory, its
+// register split, clusters of more than 8 CTAs.
+template <auto KERN>
+ttcd_status prepare_kernel(const Ctx& c, int smem, int threads, const RegSplit* split,
+                           bool wide_cluster = false) {
+  static std::atomic<uint64_t> ready{0};  // one bit per device
+  const uint64_t bit = 1ull << c.dev;
+  if (ready.load(std::memory_order_acquire) & bit) return TTCD_OK;
+  const void* k = reinterpret_cast<const void*>(KERN);
+  if (smem > 0 &&
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return TTCD_ERR_CUDA;
+  if (wide_cluster &&
+      cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return TTCD_ERR_CUDA;
+  if (split) {
+    const ttcd_status rs = check_reg_split(k, threads, *split);
+    if (rs != TTCD_OK) return rs;
+  }
+  ready.fetch_or(bit, std::memory_order_release);
+  return TTCD_OK;
 }
 
 // Process-wide diagnostic counter of kernel launches (atomic; not call state).
@@ -2713,7 +2738,8 @@ int pick_splits(long long units, int sms, long long key_tiles) {
 template <int HD, bool PAGED>
 ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const void* v,
                             const PagedCache& pc, const Ragged& rg, void* o, float* lse, int B,
-                            int T, int Hq, int Hkv, int window, int n_sink, float scale) {
+                            int T, int Hq, int Hkv, int window, int n_sink, float scale,
+                            int min_q = 1) {
   using bf = __nv_bfloat16;
   const int G = Hq / Hkv, tpt = ATT_BM / G;
   const cuuint64_t rows = PAGED ? rg.total_q : static_cast<cuuint64_t>(B) * T;
@@ -2757,6 +2783,7 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   a.tpt = tpt;
   a.window = window;
   a.n_sink = n_sink;
+  a.min_q = min_q;
   a.scale_log2 = scale * 1.4426950408889634f;
   const long long items = static_cast<long long>(a.n_units) * Hkv * (PAGED ? 1 : B);
   const long long keys = std::min<long long>(
@@ -2765,11 +2792,9 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   a.splits = pick_splits(items, c.sms, (keys + ATT_BN - 1) / ATT_BN);
   const long long grid = items * a.splits;
   if (grid >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
-  auto kern = sink_window_attn_kernel<HD, PAGED>;
+  constexpr auto kern = sink_window_attn_kernel<HD, PAGED>;
   constexpr int smem = SinkCfg<HD>::SMEM;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return TTCD_ERR_CUDA;
-  TTCD_TRY(check_reg_split(reinterpret_cast<const void*>(kern), ATT_THREADS, kAttnRegSplit));
+  TTCD_TRY(prepare_kernel<kern>(c, smem, ATT_THREADS, &kAttnRegSplit));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(ATT_THREADS);
@@ -2788,6 +2813,88 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   }
   TTCD_CHECK_LAUNCH();
   return TTCD_OK;
+}
+
+// Few rows over a paged cache.  `beside`: the tiled kernel before it in the
+// stream takes the sequences of more than one unit, and this kernel may start
+// before that one has ended.
+//
+// Clusters: as many CTAs as make four times what the GPU holds at once (4 per SM),
+// so that the last ones to run are a small part of all, while each of their
+// warps keeps four tiles of 16 keys or more.
+template <int HD, int ROWS>
+ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& pc,
+                                const Ragged& rg, void* o, float* lse, int Hq, int window,
+                                int n_sink, float scale, bool beside) {
+  PagedDecodeArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.pc = pc;
+  a.rg = rg;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.Hq = Hq;
+  a.G = Hq / pc.Hkv;
+  a.tpt = ROWS / a.G;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.only_small = beside;
+  const long long units = static_cast<long long>(rg.n_seq) * pc.Hkv;
+  const long long keys = std::min<long long>(static_cast<long long>(window) + a.tpt + n_sink,
+                                             static_cast<long long>(pc.max_pages) << pc.page_log2);
+  const long long want = std::min((16ll * c.sms + units - 1) / units, keys / (16 * 4 * PDEC_WARPS));
+  a.splits = 1;
+  while (a.splits < 16 && a.splits < want) a.splits *= 2;
+  const long long slots =
+      rg.n_seq + (beside ? 0ll : static_cast<long long>(extra_slot(rg.total_q, a.tpt)));
+  const long long grid = slots * pc.Hkv * a.splits;
+  if (grid >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
+  constexpr auto kern = paged_decode_kernel<HD, ROWS>;
+  TTCD_TRY(prepare_kernel<kern>(c, 0, PDEC_THREADS, nullptr, true));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(PDEC_THREADS);
+  cfg.stream = c.s;
+  cudaLaunchAttribute attr[2];
+  if (a.splits > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(a.splits);
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  if (beside) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  if (cudaLaunchKernelEx(&cfg, kern, a, c.st.err) != cudaSuccess) {
+    cudaGetLastError();
+    return TTCD_ERR_CUDA;
+  }
+  TTCD_CHECK_LAUNCH();
+  return TTCD_OK;
+}
+
+// The paged attention.  A sequence whose new tokens times group heads fill at
+// most one unit of 16 rows (8 for groups of up to 8) is read by the kernel of few
+// rows, others by the tiled kernel; a batch of both takes both kernels, side by
+// side.  Groups of more than 16 heads fill the tiles of the latter with one token.
+template <int HD>
+ttcd_status launch_paged(const Ctx& c, const void* q, const PagedCache& pc, const Ragged& rg,
+                         void* o, float* lse, int max_q, int Hq, int window, int n_sink,
+                         float scale) {
+  const int G = Hq / pc.Hkv;
+  const long long rows = static_cast<long long>(G) * max_q;
+  if (G <= 8 && rows <= 8)
+    return launch_paged_decode<HD, 8>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, false);
+  if (G <= 16 && rows <= 16)
+    return launch_paged_decode<HD, 16>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, false);
+  const int unit = G <= 8 ? 8 / G : 16 / G;  // tokens; 0: no kernel of few rows
+  TTCD_TRY((launch_sink_fwd<HD, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, pc.Hkv,
+                                      window, n_sink, scale, unit + 1)));
+  if (unit == 0) return TTCD_OK;
+  return G <= 8 ? launch_paged_decode<HD, 8>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, true)
+                : launch_paged_decode<HD, 16>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, true);
 }
 
 // The backward's items: query tiles, key tiles, and the query tiles past the
@@ -2864,14 +2971,11 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   if (!make_map_nd(&mq, q, 4, qd, qs, qb) || !make_map_nd(&mdo, d_o, 4, qd, qs, qb) ||
       !make_map_nd(&mk, k, 4, kd, ks, kb) || !make_map_nd(&mv, v, 4, kd, ks, kb))
     return TTCD_ERR_CUDA;
-  auto kq = sink_attn_dq_kernel<HD>;
-  auto kk = sink_attn_dkv_kernel<HD>;
+  constexpr auto kq = sink_attn_dq_kernel<HD>;
+  constexpr auto kk = sink_attn_dkv_kernel<HD>;
   constexpr int smem_q = SinkDqCfg<HD>::SMEM, smem_k = SinkDkvCfg<HD>::SMEM;
-  if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q) != cudaSuccess ||
-      cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_k) != cudaSuccess)
-    return TTCD_ERR_CUDA;
-  TTCD_TRY(check_reg_split(reinterpret_cast<const void*>(kq), ATTB_THREADS, kAttnRegSplit));
-  TTCD_TRY(check_reg_split(reinterpret_cast<const void*>(kk), ATTB_THREADS, kAttnRegSplit));
+  TTCD_TRY(prepare_kernel<kq>(c, smem_q, ATTB_THREADS, &kAttnRegSplit));
+  TTCD_TRY(prepare_kernel<kk>(c, smem_k, ATTB_THREADS, &kAttnRegSplit));
   kq<<<static_cast<unsigned>(grid_q), ATTB_THREADS, smem_q, c.s>>>(mk, mv, a, c.st);
   TTCD_CHECK_LAUNCH();
   kk<<<static_cast<unsigned>(grid_k), ATTB_THREADS, smem_k, c.s>>>(mq, mk, mv, mdo, a, c.st);
@@ -3003,9 +3107,9 @@ ttcd_status ttcd_paged_window_attn(const void* q, const void* k_pages, const voi
                       max_pages, n_pages, log2_of(page_size), Hkv};
   const Ragged rg{q_start, kv_len, n_seq, total_q};
   switch (hd) {
-    case 32: return launch_sink_fwd<32, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, Hkv, w, n_sink, sc);
-    case 64: return launch_sink_fwd<64, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, Hkv, w, n_sink, sc);
-    default: return launch_sink_fwd<128, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, Hkv, w, n_sink, sc);
+    case 32: return launch_paged<32>(c, q, pc, rg, o, lse, max_q, Hq, w, n_sink, sc);
+    case 64: return launch_paged<64>(c, q, pc, rg, o, lse, max_q, Hq, w, n_sink, sc);
+    default: return launch_paged<128>(c, q, pc, rg, o, lse, max_q, Hq, w, n_sink, sc);
   }
 }
 
