@@ -358,36 +358,9 @@ __global__ void __launch_bounds__(PDEC_THREADS, ROWS * HD <= 1024 ? (HD == 128 ?
     const uint32_t ml_addr = smem_u32(ml_cta), part_addr = smem_u32(part);
     for (int it = rank * PDEC_THREADS + threadIdx.x; it < n_rows * QV; it += a.splits * PDEC_THREADS) {
       const int r = it / QV, c = it % QV;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      float top = -INFINITY, sum = 0.f;
-      for (int c0 = 0; c0 < a.splits; c0 += 4) {  // four CTAs' parts in flight
-        float2 s[4];
-        float4 y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int from = min(c0 + u, a.splits - 1);
-          s[u] = ld_cluster_f32x2(mapa_shared(ml_addr + 8 * r, from));
-          y[u] = ld_cluster_f32x4(mapa_shared(part_addr + (r * (HD + 4) + 4 * c) * 4, from));
-          if (c0 + u >= a.splits) s[u].x = -INFINITY;
-        }
-        const float g = fmaxf(fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x)), top);
-        const float al = top == -INFINITY ? 0.f : ex2_approx(top - g);
-        sum *= al;
-        x.x *= al;
-        x.y *= al;
-        x.z *= al;
-        x.w *= al;
-        top = g;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float f = s[u].x == -INFINITY ? 0.f : ex2_approx(s[u].x - top);
-          sum = fmaf(f, s[u].y, sum);
-          x.x = fmaf(f, y[u].x, x.x);
-          x.y = fmaf(f, y[u].y, x.y);
-          x.z = fmaf(f, y[u].z, x.z);
-          x.w = fmaf(f, y[u].w, x.w);
-        }
-      }
+      float4 x;
+      float top, sum;
+      merge_parts(ml_addr + 8 * r, part_addr + (r * (HD + 4) + 4 * c) * 4, a.splits, x, top, sum);
       store(r, c, x, top, sum);
     }
     __syncwarp();

@@ -38,6 +38,9 @@
 
 namespace ttcd {
 
+constexpr int SINKB_THREADS = 640;
+constexpr int SINKB_ROWS = 512;  // element threads: (TMEM lane, quarter of the columns)
+
 struct SinkBwdArgs {
   const __nv_bfloat16* q;    // [B, T, Hq, HD]
   const __nv_bfloat16* o;
@@ -62,8 +65,8 @@ struct SinkDqCfg {
   static constexpr int KS = 3, VS = 3;
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = KS * TILE;
-  static constexpr int DEL_OFF = V_OFF + VS * TILE;  // 128 floats
-  static constexpr int BAR_OFF = DEL_OFF + 512;
+  static constexpr int DEL_OFF = V_OFF + VS * TILE;  // 2 x 128 floats
+  static constexpr int BAR_OFF = DEL_OFF + 1024;
   static constexpr int SMEM_RAW = 1024 + BAR_OFF + 256;
   // at least 120 KB: one CTA per SM (it takes all 512 TMEM columns)
   static constexpr int SMEM = SMEM_RAW > 122880 ? SMEM_RAW : 122880;
@@ -83,15 +86,15 @@ struct SinkDkvCfg {
   static constexpr int SMEM = SMEM_RAW > 122880 ? SMEM_RAW : 122880;
 };
 
-// p = 2^(s scale_log2 + nl) of 64 scores; nl per pair of columns.  One pair in
-// four on the FMA pipe where `fine` (as the forward).
-template <bool FINE, class NL>
-__device__ __forceinline__ void probs64(float (&s)[64], float scale_log2, NL nl) {
+// p = 2^(s scale_log2 + nl) of 32 scores; nl per pair of columns.  One pair in
+// four on the FMA pipe, as the forward (there a masked score gives 2^-126).
+template <class NL>
+__device__ __forceinline__ void probs32(float (&s)[32], float scale_log2, NL nl) {
   const uint64_t sc2 = f2pack(scale_log2, scale_log2);
 #pragma unroll
-  for (int c = 0; c < 64; c += 2) {
+  for (int c = 0; c < 32; c += 2) {
     const uint64_t x = fma2(f2pack(s[c], s[c + 1]), sc2, nl(c));
-    if (FINE && ((c >> 1) & 3) == 3) {
+    if (((c >> 1) & 3) == 3) {
       f2unpack(exp2_poly2_fine(x), s[c], s[c + 1]);
     } else {
       float x0, x1;
@@ -106,11 +109,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t pack2(uint64_t x) {
-  float a, b;
-  f2unpack(x, a, b);
-  return pack_bf16x2(a, b);
-}
 // dS of 32 columns: p (dp + nd), packed bf16 pairs.
 template <class ND>
 __device__ __forceinline__ void ds32(const float* p, const float (&dp)[32], ND nd, uint32_t* out) {
@@ -120,7 +118,7 @@ __device__ __forceinline__ void ds32(const float* p, const float (&dp)[32], ND n
 }
 
 template <int HD>
-__global__ void __launch_bounds__(ATTB_THREADS, 1)
+__global__ void __launch_bounds__(SINKB_THREADS, 1)
     sink_attn_dq_kernel(const __grid_constant__ CUtensorMap mapK,
                         const __grid_constant__ CUtensorMap mapV, const SinkBwdArgs a,
                         const DevStatus st) {
@@ -138,11 +136,11 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
   uint64_t* k_empty = k_full + KS;     // KS
   uint64_t* v_full = k_empty + KS;     // VS
   uint64_t* v_empty = v_full + VS;     // VS
-  uint64_t* a_ready = v_empty + VS;    // Q and dO are in TMEM (256 arrivals)
+  uint64_t* a_ready = v_empty + VS;    // Q and dO are in TMEM (every element thread arrives)
   uint64_t* s_full = a_ready + 1;
-  uint64_t* s_free = s_full + 1;       // 256 arrivals
+  uint64_t* s_free = s_full + 1;       // every element thread arrives
   uint64_t* dp_full = s_free + 1;
-  uint64_t* ds_ready = dp_full + 1;    // 256 arrivals
+  uint64_t* ds_ready = dp_full + 1;    // every element thread arrives
   uint64_t* done = ds_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -162,7 +160,7 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (uint64_t* p = bars; p <= done; ++p)
-      mbar_init(p, p == a_ready || p == s_free || p == ds_ready ? 256 : 1);
+      mbar_init(p, p == a_ready || p == s_free || p == ds_ready ? SINKB_ROWS : 1);
     *abort = 0;
     fence_mbar_init();
     tma_prefetch_map(&mapK);
@@ -176,9 +174,9 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // 128 x 56 + 256 x 224 = 384 x 168 registers
+  // 128 x 64 + 512 x 104 = 640 x 96 registers
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
     if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------- TMA producer
       int issued_k = 0, issued_v = 0;
@@ -210,11 +208,7 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
       const uint32_t v_lo = sdesc_lo(smem_u32(smem + Cfg::V_OFF), 16);
       const uint32_t k_mn = sdesc_lo(smem_u32(smem + Cfg::K_OFF), PANEL);
       auto koff = [](int kk) { return static_cast<uint32_t>(((kk >> 2) * PANEL + (kk & 3) * 32) >> 4); };
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, st, abort));
-        tc_fence_after();
-        return ok;
-      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, st, abort); };
       auto issue_s = [&](int v) {  // S = Q K^T
         const uint32_t kb = k_lo + (((v % KS) * Cfg::TILE) >> 4);
         if (elect_one()) {
@@ -250,10 +244,10 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
         }
         if (!wait(ds_ready, v & 1)) break;
         const uint32_t kb = k_mn + (((v % KS) * Cfg::TILE) >> 4);
-        if (elect_one()) {  // dQ += dS K; the halves of dS over the halves of dP
+        if (elect_one()) {  // dQ += dS K; the quarters of dS over those of dP
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts_lh(tmem + C_DQ, tmem + C_DP + (kk >> 2) * 64 + (kk & 3) * 8,
+            mma_bf16_ts_lh(tmem + C_DQ, tmem + C_DP + (kk >> 1) * 32 + (kk & 1) * 8,
                            kb + ((kk * 2048) >> 4), HI, ID_DQ, (v > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&k_empty[v % KS]);
         }
@@ -269,9 +263,9 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
       mbar_wait(done, 0, st, &no_abort);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
     // --------------------------------------------------------------- query rows
-    const int h = (warp - 4) >> 2;  // half of the columns
+    const int qd = (warp - 4) >> 2;  // quarter of the columns
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const int tok = r / a.G, head = hk * a.G + r % a.G;
@@ -282,25 +276,29 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
     float* rows = a.rows + ((static_cast<long long>(b) * a.Hkv + hk) * a.n_qt + qt) * 256;
     float nl = 0.f;
     if (row_ok) nl = -a.lse[(static_cast<long long>(b) * a.Hq + head) * a.T + t] * 1.4426950408889634f;
-    {  // this row of Q (first half) or dO (second half) into TMEM; rows that are not there: zeros
-      uint32_t w[HD / 2];
-      const uint4* src = reinterpret_cast<const uint4*>((h ? a.d_o : a.q) + row * HD);
+    {  // half a row of Q (quarters 0, 1) or dO (2, 3) into TMEM; rows that are not there: zeros
+      constexpr int W = HD / 4;  // words
+      const int half = qd & 1;
+      uint32_t w[W];
+      const uint4* src = reinterpret_cast<const uint4*>((qd >= 2 ? a.d_o : a.q) + row * HD + half * (HD / 2));
 #pragma unroll
-      for (int i = 0; i < HD / 8; ++i) {
+      for (int i = 0; i < W / 4; ++i) {
         const uint4 x = row_ok ? src[i] : make_uint4(0, 0, 0, 0);
         w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
       }
-#pragma unroll
-      for (int c = 0; c < HD / 2; c += 32)
-        tmem_st32(tmem + lane_off + (h ? C_DO : C_Q) + c, *reinterpret_cast<uint32_t(*)[32]>(&w[c]));
+      const uint32_t at = tmem + lane_off + (qd >= 2 ? C_DO : C_Q) + half * W;
+      if constexpr (W == 32)
+        tmem_st32(at, w);
+      else
+        tmem_st16(at, w);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(a_ready);
-      if (h) {
-        const uint4* os = reinterpret_cast<const uint4*>(a.o + row * HD);
+      if (qd >= 2) {
+        const uint4* os = reinterpret_cast<const uint4*>(a.o + row * HD + half * (HD / 2));
         float d = 0.f;
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
+        for (int i = 0; i < W / 4; ++i) {
           const uint4 x = row_ok ? os[i] : make_uint4(0, 0, 0, 0);
           const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -309,61 +307,58 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
             d = fmaf(bf16hi_to_f32(u[e]), bf16hi_to_f32(w[4 * i + e]), d);
           }
         }
-        del[r] = -d;
-        rows[128 + r] = -d;
-      } else {
-        rows[r] = row_ok ? nl : -INFINITY;
+        del[half * 128 + r] = -d;
       }
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const uint64_t nd2 = f2pack(del[r], del[r]), nl2 = f2pack(nl, nl);
-    const uint32_t s_addr = tmem + lane_off + C_S + 64 * h, dp_addr = tmem + lane_off + C_DP + 64 * h;
+    asm volatile("bar.sync 1, 512;" ::: "memory");
+    const float nd = del[r] + del[128 + r];
+    if (qd == 0) rows[r] = row_ok ? nl : -INFINITY;
+    if (qd == 1) rows[128 + r] = nd;
+    const uint64_t nd2 = f2pack(nd, nd), nl2 = f2pack(nl, nl);
+    const uint32_t s_addr = tmem + lane_off + C_S + 32 * qd, dp_addr = tmem + lane_off + C_DP + 32 * qd;
     bool ok = true;
     for (int v = 0; v < nv; ++v) {
       const int k0 = key_tile(v) * 128;
-      if (!mbar_wait(s_full, v & 1, st, abort)) { ok = false; break; }
-      tc_fence_after();
-      float p[64];
-      tmem_ld_cols<64>(s_addr, p);
+      if (!warp_wait(s_full, v & 1, st, abort)) { ok = false; break; }
+      float p[32];
+      tmem_ld32f(s_addr, p);
       tc_fence_before();
       mbar_arrive(s_free);
       const bool unmasked =
           k0 + 127 <= t0 && (k0 > t1 - a.window || k0 + 128 <= a.n_sink);
-      if (unmasked) {
-        probs64<true>(p, a.scale_log2, [&](int) { return nl2; });
-      } else {
-        const int c0 = k0 + 64 * h;
+      if (!unmasked) {
+        const int c0 = k0 + 32 * qd;
         const int hi = t - c0, lo = t - a.window + 1 - c0, ns = a.n_sink - c0;
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < 32; ++c)
           p[c] = (c <= hi && (c >= lo || c < ns)) ? p[c] : -INFINITY;
-        probs64<false>(p, a.scale_log2, [&](int) { return nl2; });
       }
-      if (!mbar_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t D[32];
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        float dp[32];
-        tmem_ld32f(dp_addr + c, dp);
-        ds32(&p[c], dp, [&](int) { return nd2; }, &D[c >> 1]);
-      }
-      tmem_st32(dp_addr, D);
+      probs32(p, a.scale_log2, [&](int) { return nl2; });
+      if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
+      uint32_t D[16];
+      float dp[32];
+      tmem_ld32f(dp_addr, dp);
+      ds32(p, dp, [&](int) { return nd2; }, D);
+      tmem_st16(dp_addr, D);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(ds_ready);
     }
-    if (ok && mbar_wait(done, 0, st, abort)) {
-      tc_fence_after();
-      // half of the row's columns each
-      __nv_bfloat16* dst = a.dq + row * HD + h * (HD / 2);
+    if (ok && warp_wait(done, 0, st, abort)) {
+      // a quarter of the row's columns each
+      __nv_bfloat16* dst = a.dq + row * HD + qd * (HD / 4);
 #pragma unroll
-      for (int c = 0; c < HD / 2; c += 32) {
-        float x[32];
-        tmem_ld32f(tmem + lane_off + C_DQ + h * (HD / 2) + c, x);
+      for (int c = 0; c < HD / 4; c += 16) {
+        uint32_t x[16];
+        tmem_ld16(tmem + lane_off + C_DQ + qd * (HD / 4) + c, x);
+        tmem_ld_wait();
+        float y[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] *= a.scale;
-        if (row_ok) store_x32(dst + c, x);
+        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(x[i]) * a.scale;
+        if (row_ok) {
+          st8f(dst + c, *reinterpret_cast<float(*)[8]>(&y[0]));
+          st8f(dst + c + 8, *reinterpret_cast<float(*)[8]>(&y[8]));
+        }
       }
     }
   }
@@ -375,7 +370,7 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
 }
 
 template <int HD>
-__global__ void __launch_bounds__(ATTB_THREADS, 1)
+__global__ void __launch_bounds__(SINKB_THREADS, 1)
     sink_attn_dkv_kernel(const __grid_constant__ CUtensorMap mapQ,
                          const __grid_constant__ CUtensorMap mapK,
                          const __grid_constant__ CUtensorMap mapV,
@@ -397,9 +392,9 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
   uint64_t* do_full = bars + 5;   // 2
   uint64_t* do_empty = bars + 7;  // 2
   uint64_t* s_full = bars + 9;
-  uint64_t* p_ready = bars + 10;  // 256 arrivals
+  uint64_t* p_ready = bars + 10;  // every element thread arrives
   uint64_t* dp_full = bars + 11;
-  uint64_t* ds_ready = bars + 12; // 256 arrivals
+  uint64_t* ds_ready = bars + 12; // every element thread arrives
   uint64_t* done = bars + 13;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -419,7 +414,7 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
   const int rows_used = a.G * a.tpt;
 
   if (threadIdx.x == 0) {
-    for (uint64_t* p = bars; p <= done; ++p) mbar_init(p, p == p_ready || p == ds_ready ? 256 : 1);
+    for (uint64_t* p = bars; p <= done; ++p) mbar_init(p, p == p_ready || p == ds_ready ? SINKB_ROWS : 1);
     *abort = 0;
     fence_mbar_init();
     tma_prefetch_map(&mapQ);
@@ -429,7 +424,7 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
   }
   // rows of the Q and dO stages that no load writes: zeros (their P is 0, and 0
   // times what lies there must be 0)
-  for (int i = threadIdx.x; i < (128 - rows_used) * 8 * Cfg::PANELS * 4; i += ATTB_THREADS) {
+  for (int i = threadIdx.x; i < (128 - rows_used) * 8 * Cfg::PANELS * 4; i += SINKB_THREADS) {
     const int c = i & 7, x = i >> 3, panel = x % (Cfg::PANELS * 4), r = rows_used + x / (Cfg::PANELS * 4);
     *reinterpret_cast<uint4*>(smem + Cfg::Q_OFF + panel * PANEL + r * 128 + c * 16) =
         make_uint4(0, 0, 0, 0);
@@ -444,7 +439,7 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
     if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------- TMA producer
       const uint32_t bytes = Cfg::PANELS * 128 * rows_used;
@@ -492,11 +487,7 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
       const uint32_t q_mn = sdesc_lo(smem_u32(smem + Cfg::Q_OFF), PANEL);
       const uint32_t do_mn = sdesc_lo(smem_u32(smem + Cfg::DO_OFF), PANEL);
       auto koff = [](int kk) { return static_cast<uint32_t>(((kk >> 2) * PANEL + (kk & 3) * 32) >> 4); };
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, st, abort));
-        tc_fence_after();
-        return ok;
-      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, st, abort); };
       auto issue_scores = [&](uint32_t d, uint32_t a_lo, uint32_t b_lo, uint64_t* bar) {
         if (elect_one()) {
 #pragma unroll
@@ -506,12 +497,12 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
         }
         __syncwarp();
       };
-      // += P^T dO or dS^T Q; the halves of the A operand over the halves of its scores
+      // += P^T dO or dS^T Q; the quarters of the A operand over those of its scores
       auto issue_acc = [&](uint32_t d, uint32_t at, uint32_t b_mn, bool first, uint64_t* bar) {
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts_lh(tmem + d, tmem + at + (kk >> 2) * 64 + (kk & 3) * 8,
+            mma_bf16_ts_lh(tmem + d, tmem + at + (kk >> 1) * 32 + (kk & 1) * 8,
                            b_mn + ((kk * 2048) >> 4), HI, ID_KV, (!first || kk > 0) ? 1u : 0u);
           mma_commit(bar);
         }
@@ -545,71 +536,64 @@ __global__ void __launch_bounds__(ATTB_THREADS, 1)
       mbar_wait(done, 0, st, &no_abort);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
     // ----------------------------------------------------------------- key rows
-    const int h = (warp - 4) >> 2;  // half of the columns
+    const int qd = (warp - 4) >> 2;  // quarter of the columns
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const int j = k0 + r;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lane_off + C_S + 64 * h, dp_addr = tmem + lane_off + C_DP + 64 * h;
+    const uint32_t s_addr = tmem + lane_off + C_S + 32 * qd, dp_addr = tmem + lane_off + C_DP + 32 * qd;
     bool ok = true;
     for (int v = 0; v < nv; ++v) {
       const int t0 = (qt0 + v) * a.tpt, t1 = t0 + a.tpt - 1;
-      if (!mbar_wait(&q_full[v & 1], (v >> 1) & 1, st, abort)) { ok = false; break; }
-      const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + Cfg::ROW_OFF + (v & 1) * 1024 + h * 256);
+      if (!warp_wait(&q_full[v & 1], (v >> 1) & 1, st, abort)) { ok = false; break; }
+      const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + Cfg::ROW_OFF + (v & 1) * 1024 + qd * 128);
       const ulonglong2* nd = nl + 32;
-      if (!mbar_wait(s_full, v & 1, st, abort)) { ok = false; break; }
-      tc_fence_after();
-      float p[64];
-      tmem_ld_cols<64>(s_addr, p);
+      if (!warp_wait(s_full, v & 1, st, abort)) { ok = false; break; }
+      float p[32];
+      tmem_ld32f(s_addr, p);
       auto pair = [](const ulonglong2* x, int c) { return (c & 2) ? x[c >> 2].y : x[c >> 2].x; };
       const bool unmasked =
           k0 + 127 <= t0 && (t1 - a.window < k0 || k0 + 128 <= a.n_sink);
-      if (unmasked) {
-        probs64<true>(p, a.scale_log2, [&](int c) { return pair(nl, c); });
-      } else {
+      if (!unmasked) {
         // columns (token, head) of the tokens from j to the last that sees it
-        const int lo = max(j - t0, 0) * a.G - 64 * h;
+        const int lo = max(j - t0, 0) * a.G - 32 * qd;
         const int last = j < a.n_sink ? 128 : min(max(j + a.window - t0, 0), 128);
-        const int hi = last * a.G - 64 * h;
+        const int hi = last * a.G - 32 * qd;
 #pragma unroll
-        for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c < hi) ? p[c] : -INFINITY;
-        probs64<false>(p, a.scale_log2, [&](int c) { return pair(nl, c); });
+        for (int c = 0; c < 32; ++c) p[c] = (c >= lo && c < hi) ? p[c] : -INFINITY;
       }
-      uint32_t P[32];
+      probs32(p, a.scale_log2, [&](int c) { return pair(nl, c); });
+      uint32_t P[16];
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) P[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
-      tmem_st32(s_addr, P);
+      for (int c = 0; c < 32; c += 2) P[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
+      tmem_st16(s_addr, P);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(p_ready);
-      if (!mbar_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        float dp[32];
-        tmem_ld32f(dp_addr + c, dp);
-        ds32(&p[c], dp, [&](int i) { return pair(nd, c + i); }, &P[c >> 1]);
-      }
-      tmem_st32(dp_addr, P);
+      if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
+      float dp[32];
+      tmem_ld32f(dp_addr, dp);
+      ds32(p, dp, [&](int i) { return pair(nd, i); }, P);
+      tmem_st16(dp_addr, P);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(ds_ready);
     }
-    // ------------------------------------------------- dK (first half), dV rows
-    if (ok && mbar_wait(done, 0, st, abort)) {
-      tc_fence_after();
-      const float f = h ? 1.f : a.scale;
+    // ------------------------------------ halves of the dK (quarters 0, 1) and dV rows
+    if (ok && warp_wait(done, 0, st, abort)) {
+      const int which = qd >> 1, col = (qd & 1) * (HD / 2);
+      const float f = which ? 1.f : a.scale;
       const bool part = a.n_far > 0 && kt == 0 && r < a.n_sink;  // a sum of several items
       const long long bh = static_cast<long long>(b) * a.Hkv + hk;
-      float* ps = a.partial +
-          ((((far ? item + 1 : 0) * static_cast<long long>(a.B) * a.Hkv + bh) * 2 + h) * a.n_sink + r) * HD;
-      __nv_bfloat16* dst = (h ? a.dv : a.dk) + ((static_cast<long long>(b) * a.T + j) * a.Hkv + hk) * HD;
+      float* ps = a.partial + col +
+          ((((far ? item + 1 : 0) * static_cast<long long>(a.B) * a.Hkv + bh) * 2 + which) * a.n_sink + r) * HD;
+      __nv_bfloat16* dst = (which ? a.dv : a.dk) + ((static_cast<long long>(b) * a.T + j) * a.Hkv + hk) * HD + col;
 #pragma unroll
-      for (int c = 0; c < HD; c += 32) {
+      for (int c = 0; c < HD / 2; c += 32) {
         float x[32];
-        tmem_ld32f(tmem + lane_off + (h ? C_DV : C_DK) + c, x);
+        tmem_ld32f(tmem + lane_off + (which ? C_DV : C_DK) + col + c, x);
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] *= f;
         if (part && j < a.T)

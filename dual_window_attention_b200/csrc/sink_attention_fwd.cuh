@@ -74,11 +74,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr)
@@ -120,6 +115,63 @@ __device__ __forceinline__ uint64_t exp2_poly2_fine(uint64_t x) {
   return f2pack(r0, r1);
 }
 
+// Four columns of a row merged over the parts of a cluster's CTAs (four parts in
+// flight): its reference maximum and sum at ml, its fp32 columns at x4, the same
+// offsets in every CTA.  A part without keys has -inf and finite columns.
+__device__ __forceinline__ void merge_parts(uint32_t ml, uint32_t x4, int parts, float4& x,
+                                            float& top, float& sum) {
+  x = make_float4(0.f, 0.f, 0.f, 0.f);
+  top = -INFINITY;
+  sum = 0.f;
+  for (int c0 = 0; c0 < parts; c0 += 4) {
+    float2 s[4];
+    float4 y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int from = min(c0 + u, parts - 1);
+      s[u] = ld_cluster_f32x2(mapa_shared(ml, from));
+      y[u] = ld_cluster_f32x4(mapa_shared(x4, from));
+      if (c0 + u >= parts) s[u].x = -INFINITY;
+    }
+    const float g = fmaxf(fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x)), top);
+    const float al = top == -INFINITY ? 0.f : ex2_approx(top - g);
+    sum *= al;
+    x.x *= al;
+    x.y *= al;
+    x.z *= al;
+    x.w *= al;
+    top = g;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float f = s[u].x == -INFINITY ? 0.f : ex2_approx(s[u].x - top);
+      sum = fmaf(f, s[u].y, sum);
+      x.x = fmaf(f, y[u].x, x.x);
+      x.y = fmaf(f, y[u].y, x.y);
+      x.z = fmaf(f, y[u].z, x.z);
+      x.w = fmaf(f, y[u].w, x.w);
+    }
+  }
+}
+
+// mbar_wait for a converged warp, the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const DevStatus& st,
+                                          volatile int* abort) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, st, abort));
+  tc_fence_after();
+  return ok;
+}
+
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  float a, b;
+  f2unpack(x, a, b);
+  return pack_bf16x2(a, b);
+}
+
+// Visits first .. first + run - 1, then (n = run + 1) `extra`.
+struct TileRange {
+  int first, run, extra, n;
+};
+
 // The positions and visits of one work unit; identical for every role.
 struct SinkVisits {
   int pos_lo[2], pos_hi[2], n[2];  // per tile; n = 0: no tile
@@ -141,6 +193,16 @@ struct SinkVisits {
     total = n_win + (all.sink_end > 0 && all.lo >= ATT_BN ? 1 : 0);
   }
   __device__ int tile(int v) const { return v < n_win ? jhi - v : 0; }
+  // the visits of [v0, v1) that tile h needs
+  __device__ TileRange range(int h, int v0, int v1) const {
+    TileRange r;
+    r.first = max(v0, jhi - j_hi[h]);
+    r.run = n[h] > 0 ? max(0, min(v1, jhi - j_lo[h] + 1) - r.first) : 0;
+    r.extra = total - 1;  // the sinks' tile
+    const bool sinks = n[h] > 0 && n_sink > 0 && j_lo[h] > 0 && tile(r.extra) == 0;
+    r.n = r.run + (sinks && r.extra >= v0 && r.extra < v1 ? 1 : 0);
+    return r;
+  }
   // whether any row of tile h sees a key of key tile j
   __device__ bool need(int h, int j) const {
     return n[h] > 0 && ((j >= j_lo[h] && j <= j_hi[h]) || (j == 0 && n_sink > 0));
@@ -435,11 +497,10 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
     float m_ref = -INFINITY, l = 0.f;
     int cnt = 0;
     bool ok = true;
-    for (int v = v0; v < v1 && ok; ++v) {
-      const int j = vis.tile(v);
-      if (!vis.need(h, j)) continue;
-      const int k0 = j * ATT_BN;
-      if (!mbar_wait(&s_full[h], cnt & 1, st, abort)) { ok = false; break; }
+    const TileRange rg = h ? vis.range(1, v0, v1) : vis.range(0, v0, v1);
+    for (int i = 0; i < rg.n; ++i) {
+      const int k0 = vis.tile(i < rg.run ? rg.first + i : rg.extra) * ATT_BN;
+      ok = mbar_wait(&s_full[h], cnt & 1, st, abort);
       ++cnt;
       tc_fence_after();
       float s[128];
@@ -466,7 +527,8 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       const float m_tile = mx * sl2;
       const bool fresh = m_ref == -INFINITY;
       const bool grow = !fresh && m_tile > m_ref + ATT_RESCALE_THRESHOLD;
-      if (__any_sync(0xffffffffu, grow)) {
+      if (__any_sync(0xffffffffu, grow || !ok)) {
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }  // a wait gave up
         const float m_new = grow ? m_tile : m_ref;
         const float al = grow ? ex2_approx(m_ref - m_new) : 1.f;
         tmem_scale_row<HD>(o_addr, al);
@@ -481,35 +543,19 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       uint64_t acc4[4] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f), f2pack(0.f, 0.f),
                           f2pack(0.f, 0.f)};
       uint32_t P[64];
-      if (unmasked) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          uint64_t x = fma2(f2pack(s[c], s[c + 1]), sc2, nm2);
-          uint64_t e;
-          if (((c >> 1) & 3) == 3) {  // one pair in four on the FMA pipe
-            e = exp2_poly2_fine(x);
-          } else {
-            float x0, x1;
-            f2unpack(x, x0, x1);
-            e = f2pack(ex2_approx(x0), ex2_approx(x1));
-          }
-          acc4[(c >> 1) & 3] = add2(acc4[(c >> 1) & 3], e);
-          float e0, e1;
-          f2unpack(e, e0, e1);
-          P[c >> 1] = pack_bf16x2(e0, e1);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          uint64_t x = fma2(f2pack(s[c], s[c + 1]), sc2, nm2);
+      for (int c = 0; c < 128; c += 2) {
+        const uint64_t x = fma2(f2pack(s[c], s[c + 1]), sc2, nm2);
+        uint64_t e;
+        if (((c >> 1) & 3) == 3) {  // one pair in four on the FMA pipe (a masked score: 2^-126)
+          e = exp2_poly2_fine(x);
+        } else {
           float x0, x1;
           f2unpack(x, x0, x1);
-          const uint64_t e = f2pack(ex2_approx(x0), ex2_approx(x1));
-          acc4[(c >> 1) & 3] = add2(acc4[(c >> 1) & 3], e);
-          float e0, e1;
-          f2unpack(e, e0, e1);
-          P[c >> 1] = pack_bf16x2(e0, e1);
+          e = f2pack(ex2_approx(x0), ex2_approx(x1));
         }
+        acc4[(c >> 1) & 3] = add2(acc4[(c >> 1) & 3], e);
+        P[c >> 1] = pack2(e);
       }
       const uint64_t acc = add2(add2(acc4[0], acc4[1]), add2(acc4[2], acc4[3]));
       float a0, a1;
@@ -542,74 +588,41 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       // are here: the operand tiles become the partial rows.
       asm volatile("bar.sync 1, 256;" ::: "memory");
       const int R = h * 128 + r;
-      float* ml = reinterpret_cast<float*>(smem + SC::ML_OFF);
+      float2* ml = reinterpret_cast<float2*>(smem + SC::ML_OFF);
       const bool part = ok && cnt > 0 && l > 0.f;
-      ml[2 * R] = part ? m_ref : -INFINITY;
-      ml[2 * R + 1] = part ? l : 0.f;
-      if (cnt > 0) {  // the same for a whole tile
-        uint8_t* mine = smem + R * SC::PITCH;
+      ml[R] = part ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
+      float* mine = reinterpret_cast<float*>(smem + R * SC::PITCH);
 #pragma unroll
-        for (int c = 0; c < HD; c += 32) {
-          float x[32];
+      for (int c = 0; c < HD; c += 32) {
+        float x[32];
+        if (cnt > 0) {  // the same for a whole tile; a tile without visits here: zeros
           tmem_ld32f(o_addr + c, x);
+        } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(mine + (c + i) * 4) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
         }
+        store_f32x32(mine + c, x);
       }
       cluster_sync_all();
       const uint32_t ml_addr = smem_u32(ml), rows_addr = smem_u32(smem);
-      constexpr int E = HD / 32;  // columns per lane
-      for (int w = rank + a.splits * (warp - 4); w < 256; w += a.splits * 8) {
-        const int hh = w >> 7, rr = w & 127;
+      constexpr int QV = HD / 4;  // float4 of a row
+      for (int it = rank * 256 + (threadIdx.x - 128); it < 256 * QV; it += a.splits * 256) {
+        const int R_ = it / QV, c = it % QV;
+        const int hh = R_ >> 7, rr = R_ & 127;
         const int tk = rr / a.G, hd_ = hk * a.G + rr % a.G;
         if (tk >= (hh ? vis.n[1] : vis.n[0])) continue;
-        float m = -INFINITY, lp = 0.f;
-        if (lane < a.splits) {
-          const float2 x = ld_cluster_f32x2(mapa_shared(ml_addr + 8 * w, lane));
-          m = x.x;
-          lp = x.y;
-        }
-        float top = m;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float wt = lp > 0.f ? ex2_approx(m - top) : 0.f;
-        float sum = wt * lp;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        float x[E] = {};
-        for (int p = 0; p < a.splits; ++p) {
-          const float wp = __shfl_sync(0xffffffffu, wt, p);
-          if (wp == 0.f) continue;
-          const uint32_t src = mapa_shared(rows_addr + w * SC::PITCH + lane * E * 4, p);
-          if constexpr (E == 4) {
-            const float4 y = ld_cluster_f32x4(src);
-            x[0] = fmaf(wp, y.x, x[0]);
-            x[1] = fmaf(wp, y.y, x[1]);
-            x[2] = fmaf(wp, y.z, x[2]);
-            x[3] = fmaf(wp, y.w, x[3]);
-          } else if constexpr (E == 2) {
-            const float2 y = ld_cluster_f32x2(src);
-            x[0] = fmaf(wp, y.x, x[0]);
-            x[1] = fmaf(wp, y.y, x[1]);
-          } else {
-            x[0] = fmaf(wp, ld_cluster_f32(src), x[0]);
-          }
-        }
+        float4 x;
+        float top, sum;
+        merge_parts(ml_addr + 8 * R_, rows_addr + R_ * SC::PITCH + 16 * c, a.splits, x, top, sum);
         const float inv = 1.f / sum;
         const int rw = q0 + tok0 + hh * a.tpt + tk;
-        __nv_bfloat16* dst = a.o + (static_cast<long long>(rw) * a.Hq + hd_) * HD + lane * E;
-        if constexpr (E == 4)
-          *reinterpret_cast<uint2*>(dst) =
-              make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-        else if constexpr (E == 2)
-          *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(x[0] * inv, x[1] * inv);
-        else
-          dst[0] = __float2bfloat16_rn(x[0] * inv);
-        if (lane == 0 && a.lse)
+        *reinterpret_cast<uint2*>(a.o + (static_cast<long long>(rw) * a.Hq + hd_) * HD + 4 * c) =
+            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+        if (c == 0 && a.lse)
           a.lse[lse_at(rw, hd_, (hh ? vis.pos_lo[1] : vis.pos_lo[0]) + tk)] =
               (top + __log2f(sum)) * 0.6931471805599453f;
       }
+      __syncwarp();
       cluster_sync_all();
     }
   }

@@ -146,6 +146,7 @@ struct RegSplit {
   int threads_high, regs_high;  // warps that take them (setmaxnreg.inc)
 };
 constexpr RegSplit kAttnRegSplit{128, 56, 256, 224};  // dual_window_attn_kernel
+constexpr RegSplit kSinkBwdRegSplit{128, 64, 512, 104};  // the sink-window backward
 constexpr RegSplit kScanRegSplit{128, 56, 256, 224};  // fastweight_scan_kernel
 constexpr RegSplit kGemm8RegSplit{128, 56, 256, 224};  // gemm_tc_kernel with 8 epilogue warps
 ttcd_status check_reg_split(const void* kern, int threads, const RegSplit& s) {
@@ -2819,9 +2820,10 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
 // stream takes the sequences of more than one unit, and this kernel may start
 // before that one has ended.
 //
-// Clusters: as many CTAs as make four times what the GPU holds at once (4 per SM),
-// so that the last ones to run are a small part of all, while each of their
-// warps keeps four tiles of 16 keys or more.
+// Clusters: CTAs for about four times what the GPU holds at once, so that the last
+// ones to run are a small part of all, while each of their warps keeps four tiles
+// of 16 keys or more.  64 sequences of 8 heads: 411, 352, 318, 348, 433 us with 1, 2,
+// 4, 8, 16 CTAs a cluster; one sequence: 119, 63, 35, 20.5, 16.4 us.
 template <int HD, int ROWS>
 ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& pc,
                                 const Ragged& rg, void* o, float* lse, int Hq, int window,
@@ -2842,9 +2844,9 @@ ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& p
   const long long units = static_cast<long long>(rg.n_seq) * pc.Hkv;
   const long long keys = std::min<long long>(static_cast<long long>(window) + a.tpt + n_sink,
                                              static_cast<long long>(pc.max_pages) << pc.page_log2);
-  const long long want = std::min((16ll * c.sms + units - 1) / units, keys / (16 * 4 * PDEC_WARPS));
+  const long long want = std::min(16ll * c.sms / units, keys / (16 * 4 * PDEC_WARPS));
   a.splits = 1;
-  while (a.splits < 16 && a.splits < want) a.splits *= 2;
+  while (a.splits < 16 && 2 * a.splits <= want) a.splits *= 2;
   const long long slots =
       rg.n_seq + (beside ? 0ll : static_cast<long long>(extra_slot(rg.total_q, a.tpt)));
   const long long grid = slots * pc.Hkv * a.splits;
@@ -2974,11 +2976,11 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   constexpr auto kq = sink_attn_dq_kernel<HD>;
   constexpr auto kk = sink_attn_dkv_kernel<HD>;
   constexpr int smem_q = SinkDqCfg<HD>::SMEM, smem_k = SinkDkvCfg<HD>::SMEM;
-  TTCD_TRY(prepare_kernel<kq>(c, smem_q, ATTB_THREADS, &kAttnRegSplit));
-  TTCD_TRY(prepare_kernel<kk>(c, smem_k, ATTB_THREADS, &kAttnRegSplit));
-  kq<<<static_cast<unsigned>(grid_q), ATTB_THREADS, smem_q, c.s>>>(mk, mv, a, c.st);
+  TTCD_TRY(prepare_kernel<kq>(c, smem_q, SINKB_THREADS, &kSinkBwdRegSplit));
+  TTCD_TRY(prepare_kernel<kk>(c, smem_k, SINKB_THREADS, &kSinkBwdRegSplit));
+  kq<<<static_cast<unsigned>(grid_q), SINKB_THREADS, smem_q, c.s>>>(mk, mv, a, c.st);
   TTCD_CHECK_LAUNCH();
-  kk<<<static_cast<unsigned>(grid_k), ATTB_THREADS, smem_k, c.s>>>(mq, mk, mv, mdo, a, c.st);
+  kk<<<static_cast<unsigned>(grid_k), SINKB_THREADS, smem_k, c.s>>>(mq, mk, mv, mdo, a, c.st);
   TTCD_CHECK_LAUNCH();
   if (p.n_far > 0) {
     const long long n = heads * 2 * n_sink * HD;
