@@ -24,11 +24,16 @@
 // their rows, which also form delta), so that shared memory is read for K and V
 // alone: 128 x 128 x 16 steps with both operands in shared memory take all of its
 // 128 bytes per cycle.  Per key tile v: S(v+1), dQ(v) += dS K, dP(v+1), with dS
-// over its dP.  It also writes -log2(e) lse and -delta of its rows, packed as the
+// over its dP.  It also writes -lse / scale and -delta of its rows, packed as the
 // tiles are, for the second kernel.
 //
 // dK/dV kernel.  Per query tile v: dV += P^T dO, S^T(v+1) = K Q^T, dK += dS^T Q,
 // dP^T(v+1) = V dO^T; P^T lies over its S^T and dS^T over its dP^T as A operands.
+// There the numbers of a query belong to a column, the same for every thread: read
+// from shared memory they cost 700 cycles of a visit's 3200, beside the products'
+// operands.  So they ride along as one more step of 16 of the two score products: the
+// key side holds 1, 1, 1, 0 ..., the query side the number as a sum of three bf16
+// (24 bits), and the scores arrive with -lse / scale and -delta in them.
 // The first key tile is seen by every query through its sinks: the query tiles
 // past its window are cut into items of their own, which write fp32 partial rows of the
 // sinks, and a last kernel adds them in a fixed order.
@@ -49,13 +54,13 @@ struct SinkBwdArgs {
   __nv_bfloat16* dq;         // [B, T, Hq, HD]
   __nv_bfloat16* dk;         // [B, T, Hkv, HD]
   __nv_bfloat16* dv;
-  float* rows;     // [B, Hkv, n_qt, 2, 128]: -log2(e) lse and -delta, packed rows
+  uint4* rows;     // [B, Hkv, n_qt, 2, 128]: -lse / scale and -delta, three bf16 each
   float* partial;  // [1 + n_far, B, Hkv, 2, n_sink, HD]: dk, dv of the sinks
   int B, T, Hq, Hkv, G, tpt, n_qt, n_kt;
   int window, n_sink;
   int n_far, far_tiles;  // items of the far queries of the sinks, query tiles each
   int far0;              // the first of these query tiles
-  float scale, scale_log2;
+  float scale, scale_log2, inv_scale;
 };
 
 template <int HD>
@@ -76,15 +81,32 @@ template <int HD>
 struct SinkDkvCfg {
   static constexpr int PANELS = HD / 64;
   static constexpr int TILE = PANELS * 128 * 128;
+  // Buffers of S^T in TMEM: two fit at head_dim 64, and the next scores form a
+  // visit ahead.
+  static constexpr int NBS = HD == 64 ? 2 : 1;
+  static constexpr int QS = NBS + 1;  // Q stages
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = TILE;
-  static constexpr int Q_OFF = 2 * TILE;   // two stages
-  static constexpr int DO_OFF = 4 * TILE;  // two stages
-  static constexpr int ROW_OFF = 6 * TILE;  // two stages of 2 x 128 floats
-  static constexpr int BAR_OFF = ROW_OFF + 2048;
+  static constexpr int Q_OFF = 2 * TILE;
+  static constexpr int DO_OFF = Q_OFF + QS * TILE;  // two stages
+  // query side of the extra step: per Q stage 128 rows of 16 bytes for S, then for dP
+  static constexpr int EXT_OFF = DO_OFF + 2 * TILE;
+  static constexpr int ONE_OFF = EXT_OFF + QS * 4096;  // its key side
+  static constexpr int ZERO_OFF = ONE_OFF + 2048;      // elements 8 .. 15 of every row
+  static constexpr int BAR_OFF = ZERO_OFF + 2048;
   static constexpr int SMEM_RAW = 1024 + BAR_OFF + 256;
   static constexpr int SMEM = SMEM_RAW > 122880 ? SMEM_RAW : 122880;
 };
+
+// x as hi + mid + lo in bf16, then zeros: 16 bytes.
+__device__ __forceinline__ uint4 split3(float x) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(x);
+  const float r = x - __bfloat162float(h);
+  const __nv_bfloat16 m = __float2bfloat16_rn(r);
+  const __nv_bfloat16 l = __float2bfloat16_rn(r - __bfloat162float(m));
+  return make_uint4(__bfloat16_as_ushort(h) | static_cast<uint32_t>(__bfloat16_as_ushort(m)) << 16,
+                    __bfloat16_as_ushort(l), 0, 0);
+}
 
 // p = 2^(s scale_log2 + nl) of 32 scores; nl per pair of columns.  One pair in
 // four on the FMA pipe, as the forward (there a masked score gives 2^-126).
@@ -273,9 +295,9 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
     const bool row_ok = tok < a.tpt && t < a.T;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const long long row = (static_cast<long long>(b) * a.T + t) * a.Hq + head;
-    float* rows = a.rows + ((static_cast<long long>(b) * a.Hkv + hk) * a.n_qt + qt) * 256;
-    float nl = 0.f;
-    if (row_ok) nl = -a.lse[(static_cast<long long>(b) * a.Hq + head) * a.T + t] * 1.4426950408889634f;
+    uint4* rows = a.rows + ((static_cast<long long>(b) * a.Hkv + hk) * a.n_qt + qt) * 256;
+    const float lse = row_ok ? a.lse[(static_cast<long long>(b) * a.Hq + head) * a.T + t] : 0.f;
+    const float nl = -lse * 1.4426950408889634f;
     {  // half a row of Q (quarters 0, 1) or dO (2, 3) into TMEM; rows that are not there: zeros
       constexpr int W = HD / 4;  // words
       const int half = qd & 1;
@@ -312,8 +334,9 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
     }
     asm volatile("bar.sync 1, 512;" ::: "memory");
     const float nd = del[r] + del[128 + r];
-    if (qd == 0) rows[r] = row_ok ? nl : -INFINITY;
-    if (qd == 1) rows[128 + r] = nd;
+    // a row that is not there: its P is 0
+    if (qd == 0) rows[r] = split3(row_ok ? -lse * a.inv_scale : -3e38f);
+    if (qd == 1) rows[128 + r] = split3(nd);
     const uint64_t nd2 = f2pack(nd, nd), nl2 = f2pack(nl, nl);
     const uint32_t s_addr = tmem + lane_off + C_S + 32 * qd, dp_addr = tmem + lane_off + C_DP + 32 * qd;
     bool ok = true;
@@ -377,25 +400,25 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
                          const __grid_constant__ CUtensorMap mapDO, const SinkBwdArgs a,
                          const DevStatus st) {
   using Cfg = SinkDkvCfg<HD>;
-  constexpr int PANEL = 128 * 128;
+  constexpr int PANEL = 128 * 128, NBS = Cfg::NBS, QS = Cfg::QS;
   constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);  // S^T, dP^T
   constexpr uint32_t ID_KV = idesc_bf16_f32(128, HD, false, true);   // dK, dV
-  constexpr uint32_t C_S = 0, C_DP = 128, C_DK = 256, C_DV = 384;
+  constexpr uint32_t C_S = 0, C_DP = NBS * 128, C_DK = C_DP + 128, C_DV = C_DK + HD;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFF);
   uint64_t* kv_full = bars;
-  uint64_t* q_full = bars + 1;    // 2 (Q and the rows' lse, delta)
-  uint64_t* q_empty = bars + 3;   // 2
-  uint64_t* do_full = bars + 5;   // 2
-  uint64_t* do_empty = bars + 7;  // 2
-  uint64_t* s_full = bars + 9;
-  uint64_t* p_ready = bars + 10;  // every element thread arrives
-  uint64_t* dp_full = bars + 11;
-  uint64_t* ds_ready = bars + 12; // every element thread arrives
-  uint64_t* done = bars + 13;
+  uint64_t* q_full = bars + 1;         // QS (Q and the extra step's rows)
+  uint64_t* q_empty = q_full + QS;     // QS
+  uint64_t* do_full = q_empty + QS;    // 2
+  uint64_t* do_empty = do_full + 2;    // 2
+  uint64_t* s_full = do_empty + 2;     // NBS
+  uint64_t* p_ready = s_full + NBS;    // NBS, every element thread arrives
+  uint64_t* dp_full = p_ready + NBS;
+  uint64_t* ds_ready = dp_full + 1;    // every element thread arrives
+  uint64_t* done = ds_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -414,7 +437,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   const int rows_used = a.G * a.tpt;
 
   if (threadIdx.x == 0) {
-    for (uint64_t* p = bars; p <= done; ++p) mbar_init(p, p == p_ready || p == ds_ready ? SINKB_ROWS : 1);
+    for (uint64_t* p = bars; p <= done; ++p) mbar_init(p, (p >= p_ready && p < dp_full) || p == ds_ready ? SINKB_ROWS : 1);
     *abort = 0;
     fence_mbar_init();
     tma_prefetch_map(&mapQ);
@@ -424,10 +447,16 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   }
   // rows of the Q and dO stages that no load writes: zeros (their P is 0, and 0
   // times what lies there must be 0)
-  for (int i = threadIdx.x; i < (128 - rows_used) * 8 * Cfg::PANELS * 4; i += SINKB_THREADS) {
-    const int c = i & 7, x = i >> 3, panel = x % (Cfg::PANELS * 4), r = rows_used + x / (Cfg::PANELS * 4);
+  constexpr int PANELS_IN = Cfg::PANELS * (QS + 2);
+  for (int i = threadIdx.x; i < (128 - rows_used) * 8 * PANELS_IN; i += SINKB_THREADS) {
+    const int c = i & 7, x = i >> 3, panel = x % PANELS_IN, r = rows_used + x / PANELS_IN;
     *reinterpret_cast<uint4*>(smem + Cfg::Q_OFF + panel * PANEL + r * 128 + c * 16) =
         make_uint4(0, 0, 0, 0);
+  }
+  if (threadIdx.x < 128) {
+    *reinterpret_cast<uint4*>(smem + Cfg::ZERO_OFF + threadIdx.x * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(smem + Cfg::ONE_OFF + threadIdx.x * 16) =
+        make_uint4(0x3f803f80u, 0x3f80u, 0, 0);  // 1, 1, 1, 0 ...
   }
   fence_async_smem();
   if (warp == 1) {
@@ -443,7 +472,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
     if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------- TMA producer
       const uint32_t bytes = Cfg::PANELS * 128 * rows_used;
-      const float* rows = a.rows + (static_cast<long long>(b) * a.Hkv + hk) * a.n_qt * 256;
+      const uint4* rows = a.rows + (static_cast<long long>(b) * a.Hkv + hk) * a.n_qt * 256;
       mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE);
 #pragma unroll
       for (int p = 0; p < Cfg::PANELS; ++p) {
@@ -452,28 +481,27 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
       }
       int issued_q = 0, issued_do = 0;
       for (int v = 0; v < nv; ++v) {
-        const int sg = v & 1, qt = qt0 + v;
-        const uint32_t ph = ((v >> 1) & 1) ^ 1;
-        if (!mbar_wait(&q_empty[sg], ph, st, abort)) break;
-        mbar_arrive_expect_tx(&q_full[sg], bytes + 1024);
+        const int sg = v % QS, so = v & 1, qt = qt0 + v;
+        if (!mbar_wait(&q_empty[sg], ((v / QS) & 1) ^ 1, st, abort)) break;
+        mbar_arrive_expect_tx(&q_full[sg], bytes + 4096);
 #pragma unroll
         for (int p = 0; p < Cfg::PANELS; ++p)
           tma_load_4d(smem + Cfg::Q_OFF + sg * Cfg::TILE + p * PANEL, &mapQ, &q_full[sg], 64 * p,
                       hk * a.G, qt * a.tpt, b);
-        bulk_load(smem + Cfg::ROW_OFF + sg * 1024, rows + qt * 256ll, 1024, &q_full[sg]);
+        bulk_load(smem + Cfg::EXT_OFF + sg * 4096, rows + qt * 256ll, 4096, &q_full[sg]);
         ++issued_q;
-        if (!mbar_wait(&do_empty[sg], ph, st, abort)) break;
-        mbar_arrive_expect_tx(&do_full[sg], bytes);
+        if (!mbar_wait(&do_empty[so], ((v >> 1) & 1) ^ 1, st, abort)) break;
+        mbar_arrive_expect_tx(&do_full[so], bytes);
 #pragma unroll
         for (int p = 0; p < Cfg::PANELS; ++p)
-          tma_load_4d(smem + Cfg::DO_OFF + sg * Cfg::TILE + p * PANEL, &mapDO, &do_full[sg], 64 * p,
+          tma_load_4d(smem + Cfg::DO_OFF + so * Cfg::TILE + p * PANEL, &mapDO, &do_full[so], 64 * p,
                       hk * a.G, qt * a.tpt, b);
         ++issued_do;
       }
       volatile int no_abort = 0;
       mbar_wait(kv_full, 0, st, &no_abort);
-      for (int j = max(0, issued_q - 2); j < issued_q; ++j)
-        mbar_wait(&q_full[j & 1], (j >> 1) & 1, st, &no_abort);
+      for (int j = max(0, issued_q - QS); j < issued_q; ++j)
+        mbar_wait(&q_full[j % QS], (j / QS) & 1, st, &no_abort);
       for (int j = max(0, issued_do - 2); j < issued_do; ++j)
         mbar_wait(&do_full[j & 1], (j >> 1) & 1, st, &no_abort);
     } else if (warp == 1) {
@@ -488,14 +516,28 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
       const uint32_t do_mn = sdesc_lo(smem_u32(smem + Cfg::DO_OFF), PANEL);
       auto koff = [](int kk) { return static_cast<uint32_t>(((kk >> 2) * PANEL + (kk & 3) * 32) >> 4); };
       auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, st, abort); };
-      auto issue_scores = [&](uint32_t d, uint32_t a_lo, uint32_t b_lo, uint64_t* bar) {
+      // the extra step: 16-byte rows, 8 rows to 128 bytes, no swizzle; elements 8 .. 15
+      // lie in the zeros
+      constexpr uint32_t HI0 = (128u >> 4) | (1u << 14);
+      const uint32_t one_lo = sdesc_lo(smem_u32(smem + Cfg::ONE_OFF), Cfg::ZERO_OFF - Cfg::ONE_OFF);
+      auto issue_scores = [&](uint32_t d, uint32_t a_lo, uint32_t b_lo, int ext, uint64_t* bar) {
+        const uint32_t e_lo = sdesc_lo(smem_u32(smem + ext), Cfg::ZERO_OFF - ext);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)
             mma_bf16_ss_lh(tmem + d, a_lo + koff(kk), HI, b_lo + koff(kk), HI, ID_S, kk > 0 ? 1u : 0u);
+          mma_bf16_ss_lh(tmem + d, one_lo, HI0, e_lo, HI0, ID_S, 1u);
           mma_commit(bar);
         }
         __syncwarp();
+      };
+      auto issue_s = [&](int v) {
+        const int sg = v % QS;
+        issue_scores(C_S + (v % NBS) * 128, k_lo, q_lo + sg * STAGE, Cfg::EXT_OFF + sg * 4096,
+                     &s_full[v % NBS]);
+      };
+      auto issue_dp = [&](int v) {
+        issue_scores(C_DP, v_lo, do_lo + (v & 1) * STAGE, Cfg::EXT_OFF + (v % QS) * 4096 + 2048, dp_full);
       };
       // += P^T dO or dS^T Q; the quarters of the A operand over those of its scores
       auto issue_acc = [&](uint32_t d, uint32_t at, uint32_t b_mn, bool first, uint64_t* bar) {
@@ -510,24 +552,27 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
       };
       bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
       if (ok) {
-        issue_scores(C_S, k_lo, q_lo, s_full);
+        issue_s(0);
         ok = wait(&do_full[0], 0);
-        if (ok) issue_scores(C_DP, v_lo, do_lo, dp_full);
+        if (ok) issue_dp(0);
+      }
+      if (ok && NBS == 2 && nv > 1) {
+        ok = wait(&q_full[1], 0);
+        if (ok) issue_s(1);
       }
       for (int v = 0; v < nv && ok; ++v) {
-        const uint32_t sg = v & 1, nx = sg ^ 1, nph = ((v + 1) >> 1) & 1;
-        const bool more = v + 1 < nv;
-        if (!wait(p_ready, v & 1)) break;
-        issue_acc(C_DV, C_S, do_mn + sg * STAGE, v == 0, &do_empty[sg]);
-        if (more) {
-          if (!wait(&q_full[nx], nph)) break;
-          issue_scores(C_S, k_lo, q_lo + nx * STAGE, s_full);
+        const uint32_t so = v & 1;
+        if (!wait(&p_ready[v % NBS], (v / NBS) & 1)) break;
+        issue_acc(C_DV, C_S + (v % NBS) * 128, do_mn + so * STAGE, v == 0, &do_empty[so]);
+        if (v + NBS < nv) {  // over the P^T that dV has just read
+          if (!wait(&q_full[(v + NBS) % QS], ((v + NBS) / QS) & 1)) break;
+          issue_s(v + NBS);
         }
         if (!wait(ds_ready, v & 1)) break;
-        issue_acc(C_DK, C_DP, q_mn + sg * STAGE, v == 0, &q_empty[sg]);
-        if (more) {
-          if (!wait(&do_full[nx], nph)) break;
-          issue_scores(C_DP, v_lo, do_lo + nx * STAGE, dp_full);
+        issue_acc(C_DK, C_DP, q_mn + (v % QS) * STAGE, v == 0, &q_empty[v % QS]);
+        if (v + 1 < nv) {
+          if (!wait(&do_full[so ^ 1], ((v + 1) >> 1) & 1)) break;
+          issue_dp(v + 1);
         }
       }
       if (elect_one()) mma_commit(done);
@@ -547,13 +592,10 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
     bool ok = true;
     for (int v = 0; v < nv; ++v) {
       const int t0 = (qt0 + v) * a.tpt, t1 = t0 + a.tpt - 1;
-      if (!warp_wait(&q_full[v & 1], (v >> 1) & 1, st, abort)) { ok = false; break; }
-      const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + Cfg::ROW_OFF + (v & 1) * 1024 + qd * 128);
-      const ulonglong2* nd = nl + 32;
-      if (!warp_wait(s_full, v & 1, st, abort)) { ok = false; break; }
+      const uint32_t s_at = s_addr + (v % NBS) * 128;
+      if (!warp_wait(&s_full[v % NBS], (v / NBS) & 1, st, abort)) { ok = false; break; }
       float p[32];
-      tmem_ld32f(s_addr, p);
-      auto pair = [](const ulonglong2* x, int c) { return (c & 2) ? x[c >> 2].y : x[c >> 2].x; };
+      tmem_ld32f(s_at, p);
       const bool unmasked =
           k0 + 127 <= t0 && (t1 - a.window < k0 || k0 + 128 <= a.n_sink);
       if (!unmasked) {
@@ -564,18 +606,19 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) p[c] = (c >= lo && c < hi) ? p[c] : -INFINITY;
       }
-      probs32(p, a.scale_log2, [&](int c) { return pair(nl, c); });
+      probs32(p, a.scale_log2, [](int) { return 0ull; });
       uint32_t P[16];
 #pragma unroll
       for (int c = 0; c < 32; c += 2) P[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
-      tmem_st16(s_addr, P);
+      tmem_st16(s_at, P);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(p_ready);
+      mbar_arrive(&p_ready[v % NBS]);
       if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
       float dp[32];
       tmem_ld32f(dp_addr, dp);
-      ds32(p, dp, [&](int i) { return pair(nd, i); }, P);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) P[c >> 1] = pack2(mul2(f2pack(p[c], p[c + 1]), f2pack(dp[c], dp[c + 1])));
       tmem_st16(dp_addr, P);
       tmem_st_wait();
       tc_fence_before();

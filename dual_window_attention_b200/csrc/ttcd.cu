@@ -2920,7 +2920,7 @@ SinkBwdPlan plan_sink_bwd(int B, int T, int Hq, int Hkv, int hd, int window, int
   }
   const size_t heads = static_cast<size_t>(B) * Hkv;
   p.rows_off = kStatusBytes;
-  p.partial_off = p.rows_off + heads * p.n_qt * 256 * sizeof(float);
+  p.partial_off = p.rows_off + heads * p.n_qt * 256 * sizeof(uint4);
   p.bytes = p.partial_off;
   if (p.n_far > 0)
     p.bytes += (1 + static_cast<size_t>(p.n_far)) * heads * 2 * n_sink * hd * sizeof(float);
@@ -2942,7 +2942,7 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   a.dq = static_cast<bf*>(dq);
   a.dk = static_cast<bf*>(dk);
   a.dv = static_cast<bf*>(dv);
-  a.rows = reinterpret_cast<float*>(static_cast<char*>(ws) + p.rows_off);
+  a.rows = reinterpret_cast<uint4*>(static_cast<char*>(ws) + p.rows_off);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.partial_off);
   a.B = B;
   a.T = T;
@@ -2959,6 +2959,7 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   a.far0 = p.far0;
   a.scale = scale;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.inv_scale = 1.f / scale;
   const long long heads = static_cast<long long>(B) * Hkv;
   const long long grid_q = heads * p.n_qt, grid_k = heads * (p.n_far + p.n_kt);
   if (grid_q >= (1ll << 31) || grid_k >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
@@ -3038,6 +3039,7 @@ ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const v
                                            int Hkv, int hd, int window, int n_sink, float scale,
                                            void* workspace, size_t ws_bytes, void* stream) {
   if (!(scale >= 0.f) || !std::isfinite(scale)) return TTCD_ERR_INVALID_ARG;
+  if (scale > 0.f && scale < 1e-30f) return TTCD_ERR_UNSUPPORTED;  // lse / scale is formed
   TTCD_TRY(check_sink_bwd(B, T, Hq, Hkv, hd, window, n_sink));
   const void* need[] = {q, k, v, o, lse, d_o, dq, dk, dv, workspace};
   for (const void* x : need)

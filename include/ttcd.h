@@ -581,7 +581,9 @@ ttcd_status ttcd_block_decode_next_ex(const void* x_t, const float* beta_t,
  *   dtype      must be TTCD_BF16 (TTCD_F32 -> TTCD_ERR_UNSUPPORTED)
  * ttcd_sink_window_attn_backward: its vector-Jacobian product for dL/do = d_o,
  *   with the formulas of ttcd_dual_window_attn_backward; hd 64 or 128 (32:
- *   TTCD_ERR_UNSUPPORTED).  P is rebuilt from the forward's lse.
+ *   TTCD_ERR_UNSUPPORTED), scale 0 or at least 1e-30 (below:
+ *   TTCD_ERR_UNSUPPORTED).  P is rebuilt from the forward's lse.  The results do
+ *   not depend on the order in which blocks run: two runs give the same bits.
  *   o, lse     the forward's outputs
  *   d_o        [B, T, Hq, hd] bf16, device
  *   dq         [B, T, Hq, hd]  bf16, device, written
