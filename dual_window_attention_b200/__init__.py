@@ -726,14 +726,13 @@ def _takes(what: str, device, **tensors) -> None:
     if device.type != "cuda":
         raise ValueError(f"{what}: libttcd takes CUDA tensors only (no CPU path)")
     for name, (t, shape, dtypes) in tensors.items():
-        if t is None:
+        if t is None or (t.get_device() == device.index and t.shape == shape and t.dtype in dtypes):
             continue
         if t.device != device:
             raise ValueError(f"{what}: {name} is on {t.device}, not on {device}")
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        if t.dtype not in dtypes:
-            raise ValueError(f"{what}: {name} is {t.dtype}")
+        raise ValueError(f"{what}: {name} is {t.dtype}")
 
 
 _F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)

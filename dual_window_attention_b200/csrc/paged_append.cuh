@@ -11,14 +11,18 @@
 // fraction of a turn there, then sincospi in 32 bits: at p = 10^6 a 32-bit
 // product alone would be off by 0.06 radians.
 //
-// Bound by DRAM: each row is read once and written once (16 bytes per thread
-// and access); the angles of a token are formed once for all its heads.
+// Bound by DRAM: each row is read once and written once (16 bytes per thread and
+// access).  One warp per token and no barrier of the block: lane l has the angles
+// 2l and 2l + 1 and hands them on through shared memory of its warp; then each
+// lane keeps the 8 angles of its chunk for all the heads, whose loads go out four
+// at a time before the first is used.
 #pragma once
 #include "sink_attention.cuh"
 
 namespace ttcd {
 
-constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_WARPS = 4;
+constexpr int APPEND_THREADS = 32 * APPEND_WARPS;
 
 struct AppendArgs {
   const __nv_bfloat16* qkv;  // [total_q, (Hq + 2 Hkv) hd]
@@ -27,98 +31,115 @@ struct AppendArgs {
   __nv_bfloat16* v_pages;
   const int* table;          // [n_seq, max_pages]
   Ragged rg;
-  int max_pages, n_pages, page_log2, Hq, Hkv, hd;
+  int max_pages, n_pages, page_log2, Hq, Hkv;
   double log2_theta;  // log2 of the base
   bool rotate;
 };
 
-// TOK tokens per block and turn of its loop.
-template <int TOK>
+template <int HD>
 __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const AppendArgs a,
                                                                       uint32_t* err) {
-  __shared__ double freq[64];       // turns per position
-  __shared__ float2 cs[TOK][64];    // cos, sin
-  __shared__ int pos[TOK];          // -1: no token here
-  __shared__ long long kv_row[TOK]; // row of (page, head 0), -1: no page
-  const int half = a.hd / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int HALF = HD / 2;
+  constexpr int LPH = HALF / 8;         // lanes per rotated head: a chunk of 8 pairs each
+  constexpr int HPW = 32 / LPH;         // rotated heads per pass of the warp
+  constexpr int VPL = HD / 8;           // chunks of a v head
+  __shared__ float2 cs_all[APPEND_WARPS][HALF];  // cos, sin
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float2* cs = cs_all[warp];
   const int page_size = 1 << a.page_log2;
-  if (threadIdx.x < half)
-    freq[threadIdx.x] =
-        exp2(-2.0 * threadIdx.x / a.hd * a.log2_theta) * 0.15915494309189533577;  // 1 / 2 pi
+  const long long cap = static_cast<long long>(a.max_pages) << a.page_log2;
   if (blockIdx.x == 0) {  // every sequence's numbers are consistent, or this call says so
-    const long long cap = static_cast<long long>(a.max_pages) << a.page_log2;
     for (int s = threadIdx.x; s < a.rg.n_seq; s += APPEND_THREADS)
       if (load_span(a.rg, s, cap).bad) atomicOr(err, DEV_ERR_BAD_INDEX);
   }
-  const int rope_units = (a.Hq + a.Hkv) * (half / 8), units = rope_units + a.Hkv * (a.hd / 8);
-  for (int row0 = blockIdx.x * TOK; row0 < a.rg.total_q; row0 += gridDim.x * TOK) {
-    if (warp < TOK) {  // whose token, where
-      const int row = row0 + warp;
-      const int s = seq_of_row(a.rg, row);
-      int p = -1;
-      long long r = -1;
-      if (s >= 0 && row < a.rg.total_q) {
-        const SeqSpan sp = load_span(a.rg, s, static_cast<long long>(a.max_pages) << a.page_log2);
-        if (row - sp.q0 < sp.n) {
-          p = sp.L - sp.n + row - sp.q0;
-          const int id = a.table[static_cast<long long>(s) * a.max_pages + (p >> a.page_log2)];
-          r = page_row(id, a.n_pages, a.Hkv, 0, page_size);
-          if (r < 0 && lane == 0) atomicOr(err, DEV_ERR_BAD_INDEX);
-        }
-      }
-      if (lane == 0) {
-        pos[warp] = p;
-        kv_row[warp] = r;
-      }
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < TOK * half; e += APPEND_THREADS) {
-      const int tk = e / half, i = e % half;
-      float2 c = make_float2(1.f, 0.f);
-      if (a.rotate && pos[tk] >= 0) {
-        const double turns = pos[tk] * freq[i];
-        sincospif(2.f * static_cast<float>(turns - rint(turns)), &c.y, &c.x);
-      }
-      cs[tk][i] = c;
-    }
-    __syncthreads();
-    for (int u = threadIdx.x; u < TOK * units; u += APPEND_THREADS) {
-      const int tk = u / units, w = u % units;
-      const int p = pos[tk];
-      if (p < 0) continue;
-      const long long row = row0 + tk;
-      const __nv_bfloat16* src = a.qkv + row * (a.Hq + 2 * a.Hkv) * a.hd;
-      const long long in_page = p & (page_size - 1);
-      if (w < rope_units) {
-        const int head = w / (half / 8), i = (w % (half / 8)) * 8;
-        float x[8], y[8];
-        ld8f(src + head * a.hd + i, x);
-        ld8f(src + head * a.hd + half + i, y);
+  // turns per position of this lane's angles
+  double freq[(HALF + 31) / 32];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 c = cs[tk][i + e];
-          const float x0 = x[e];
-          x[e] = x0 * c.x - y[e] * c.y;
-          y[e] = y[e] * c.x + x0 * c.y;
+  for (int i = 0; i < (HALF + 31) / 32; ++i)
+    freq[i] = exp2(-2.0 * (lane + 32 * i) / HD * a.log2_theta) * 0.15915494309189533577;  // 1 / 2 pi
+  const int c = lane % LPH, h0 = lane / LPH;
+  const int n_rot = a.Hq + a.Hkv;
+  for (int row = blockIdx.x * APPEND_WARPS + warp; row < a.rg.total_q;
+       row += gridDim.x * APPEND_WARPS) {
+    const __nv_bfloat16* src = a.qkv + static_cast<long long>(row) * (a.Hq + 2 * a.Hkv) * HD;
+    // the first rotated heads' loads go out before the token's place is known
+    uint4 lo[4], hi[4];
+    auto load = [&](int first) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int head = first + u * HPW + h0;
+        if (head < n_rot) {
+          lo[u] = *reinterpret_cast<const uint4*>(src + head * HD + c * 8);
+          hi[u] = *reinterpret_cast<const uint4*>(src + head * HD + HALF + c * 8);
         }
-        __nv_bfloat16* dst;
-        if (head < a.Hq) {
-          dst = a.q_out + (row * a.Hq + head) * a.hd;
-        } else {
-          if (kv_row[tk] < 0) continue;
-          dst = a.k_pages +
-                (kv_row[tk] + static_cast<long long>(head - a.Hq) * page_size + in_page) * a.hd;
+      }
+    };
+    load(0);
+    const int s = seq_of_row(a.rg, row);
+    if (s < 0) continue;
+    const SeqSpan sp = load_span(a.rg, s, cap);
+    if (row - sp.q0 >= sp.n) continue;  // padding, or a sequence that cannot be
+    const int p = sp.L - sp.n + row - sp.q0;
+    const int id = a.table[static_cast<long long>(s) * a.max_pages + (p >> a.page_log2)];
+    const long long kv_row = page_row(id, a.n_pages, a.Hkv, 0, page_size);
+    if (kv_row < 0 && lane == 0) atomicOr(err, DEV_ERR_BAD_INDEX);
+    const long long kv_at = (kv_row + (p & (page_size - 1))) * HD;  // of head 0
+    __syncwarp();  // the previous token's angles have been read
+#pragma unroll
+    for (int i = 0; i < (HALF + 31) / 32; ++i)
+      if (lane + 32 * i < HALF) {
+        float2 x = make_float2(1.f, 0.f);
+        if (a.rotate) {
+          const double turns = p * freq[i];
+          sincospif(2.f * static_cast<float>(turns - rint(turns)), &x.y, &x.x);
         }
-        st8f(dst + i, x);
-        st8f(dst + half + i, y);
-      } else if (kv_row[tk] >= 0) {
-        const int head = (w - rope_units) / (a.hd / 8), i = ((w - rope_units) % (a.hd / 8)) * 8;
-        *reinterpret_cast<uint4*>(
-            a.v_pages + (kv_row[tk] + static_cast<long long>(head) * page_size + in_page) * a.hd + i) =
-            *reinterpret_cast<const uint4*>(src + (a.Hq + a.Hkv + head) * a.hd + i);
+        cs[lane + 32 * i] = x;
+      }
+    __syncwarp();
+    float2 rot[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rot[e] = cs[c * 8 + e];
+    for (int first = 0; first < n_rot; first += 4 * HPW) {
+      if (first > 0) load(first);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int head = first + u * HPW + h0;
+        if (head >= n_rot || (head >= a.Hq && kv_row < 0)) continue;
+        const uint32_t xw[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w};
+        const uint32_t yw[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+        uint32_t xo[4], yo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x0 = bf16lo_to_f32(xw[e]), x1 = bf16hi_to_f32(xw[e]);
+          const float y0 = bf16lo_to_f32(yw[e]), y1 = bf16hi_to_f32(yw[e]);
+          const float2 r0 = rot[2 * e], r1 = rot[2 * e + 1];
+          xo[e] = pack_bf16x2(x0 * r0.x - y0 * r0.y, x1 * r1.x - y1 * r1.y);
+          yo[e] = pack_bf16x2(y0 * r0.x + x0 * r0.y, y1 * r1.x + x1 * r1.y);
+        }
+        __nv_bfloat16* dst =
+            head < a.Hq ? a.q_out + (static_cast<long long>(row) * a.Hq + head) * HD
+                        : a.k_pages + kv_at + static_cast<long long>(head - a.Hq) * page_size * HD;
+        *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(xo[0], xo[1], xo[2], xo[3]);
+        *reinterpret_cast<uint4*>(dst + HALF + c * 8) = make_uint4(yo[0], yo[1], yo[2], yo[3]);
       }
     }
-    __syncthreads();  // the tables are free for the next tokens
+    if (kv_row >= 0) {
+      const __nv_bfloat16* vs = src + n_rot * HD;
+      for (int u0 = lane; u0 < a.Hkv * VPL; u0 += 4 * 32) {
+        uint4 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u0 + 32 * u < a.Hkv * VPL) w[u] = *reinterpret_cast<const uint4*>(vs + (u0 + 32 * u) * 8);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int x = u0 + 32 * u;
+          if (x < a.Hkv * VPL)
+            *reinterpret_cast<uint4*>(a.v_pages + kv_at +
+                                      static_cast<long long>(x / VPL) * page_size * HD +
+                                      (x % VPL) * 8) = w[u];
+        }
+      }
+    }
   }
 }
 

@@ -62,12 +62,6 @@ __device__ __forceinline__ void ld_stream(uint32_t (&r)[2], const void* p) {
                : "l"(p));
 }
 
-// Waits for the kernels before this one in a programmatic launch (otherwise they
-// have ended anyway).
-__device__ __forceinline__ void grid_dep_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // ROWS: 8 or 16 query rows of a unit (the tensor instruction has 16 either way;
 // with 8 the registers of the others are free).
 template <int HD, int ROWS>

@@ -69,4 +69,25 @@ __device__ __forceinline__ int seq_of_row(const Ragged& r, int row) {
   return last;
 }
 
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+// Keeps the scores of N columns (a multiple of 32) whose bit is set, the others
+// become -inf; word(k) has the bits of the columns 32 k ...: two instructions per
+// score, where the comparisons themselves would be six.
+template <int N, class Word>
+__device__ __forceinline__ void mask_scores(float (&s)[N], Word word) {
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) {
+    const uint32_t w = word(k);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[32 * k + i] = (w >> i) & 1u ? s[32 * k + i] : -INFINITY;
+  }
+}
+// The columns of keys k0 .. k0 + 31 that the query at t sees.
+__device__ __forceinline__ uint32_t seen_bits(int t, int k0, int window, int n_sink) {
+  return low_bits(t + 1 - k0) & (~low_bits(t - window + 1 - k0) | low_bits(n_sink - k0));
+}
+
 }  // namespace ttcd

@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
                         const __grid_constant__ CUtensorMap mapV, const SinkBwdArgs a,
                         const DevStatus st) {
   using Cfg = SinkDqCfg<HD>;
+  grid_dep_launch();  // the dK/dV kernel's CTAs may set up beside the last of these
   constexpr int KS = Cfg::KS, VS = Cfg::VS, PANEL = 128 * 128;
   constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);  // S, dP
   constexpr uint32_t ID_DQ = idesc_bf16_f32(128, HD, false, true);
@@ -349,13 +350,8 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
       mbar_arrive(s_free);
       const bool unmasked =
           k0 + 127 <= t0 && (k0 > t1 - a.window || k0 + 128 <= a.n_sink);
-      if (!unmasked) {
-        const int c0 = k0 + 32 * qd;
-        const int hi = t - c0, lo = t - a.window + 1 - c0, ns = a.n_sink - c0;
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          p[c] = (c <= hi && (c >= lo || c < ns)) ? p[c] : -INFINITY;
-      }
+      if (!unmasked)
+        mask_scores(p, [&](int) { return seen_bits(t, k0 + 32 * qd, a.window, a.n_sink); });
       probs32(p, a.scale_log2, [&](int) { return nl2; });
       if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
       uint32_t D[16];
@@ -400,6 +396,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
                          const __grid_constant__ CUtensorMap mapDO, const SinkBwdArgs a,
                          const DevStatus st) {
   using Cfg = SinkDkvCfg<HD>;
+  grid_dep_launch();
   constexpr int PANEL = 128 * 128, NBS = Cfg::NBS, QS = Cfg::QS;
   constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);  // S^T, dP^T
   constexpr uint32_t ID_KV = idesc_bf16_f32(128, HD, false, true);   // dK, dV
@@ -479,6 +476,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         tma_load_4d(smem + Cfg::K_OFF + p * PANEL, &mapK, kv_full, 64 * p, hk, k0, b);
         tma_load_4d(smem + Cfg::V_OFF + p * PANEL, &mapV, kv_full, 64 * p, hk, k0, b);
       }
+      grid_dep_wait();  // the rows' numbers are the dQ kernel's
       int issued_q = 0, issued_do = 0;
       for (int v = 0; v < nv; ++v) {
         const int sg = v % QS, so = v & 1, qt = qt0 + v;
@@ -603,8 +601,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         const int lo = max(j - t0, 0) * a.G - 32 * qd;
         const int last = j < a.n_sink ? 128 : min(max(j + a.window - t0, 0), 128);
         const int hi = last * a.G - 32 * qd;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) p[c] = (c >= lo && c < hi) ? p[c] : -INFINITY;
+        mask_scores(p, [&](int) { return low_bits(hi) & ~low_bits(lo); });
       }
       probs32(p, a.scale_log2, [](int) { return 0ull; });
       uint32_t P[16];
@@ -657,6 +654,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
 // One thread per element; T > n_sink wherever there are far items.
 template <int HD>
 __global__ void sink_attn_join_kernel(const SinkBwdArgs a) {
+  grid_dep_wait();
   const long long per = static_cast<long long>(a.B) * a.Hkv * 2 * a.n_sink * HD;
   const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= per) return;

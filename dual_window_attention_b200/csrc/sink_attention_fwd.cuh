@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
   int* unit = reinterpret_cast<int*>(tmem_slot + 2);  // paged: sequence, first token, span
 
   // the kernel of the short sequences may start beside the last of these CTAs
-  if (PAGED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (PAGED) grid_dep_launch();
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -508,12 +508,8 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       // every row of the tile sees the whole key tile
       const bool unmasked = k0 + ATT_BN - 1 <= p_lo &&
                             (k0 > p_hi - a.window || k0 + ATT_BN <= a.n_sink);
-      if (!unmasked) {
-        const int hi = t - k0, lo = t - a.window + 1 - k0, ns = a.n_sink - k0;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          s[c] = (c <= hi && (c >= lo || c < ns)) ? s[c] : -INFINITY;
-      }
+      if (!unmasked)
+        mask_scores(s, [&](int k) { return seen_bits(t, k0 + 32 * k, a.window, a.n_sink); });
       // row maximum as four independent chains (short dependency latency)
       float mx4[4];
 #pragma unroll

@@ -2728,6 +2728,29 @@ bool make_map_nd(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* di
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may begin before the kernel before it has ended; the new kernel
+// waits for it itself (grid_dep_wait).
+template <class... Args>
+ttcd_status launch_programmatic(void (*kern)(Args...), long long grid, int threads, int smem,
+                                cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return TTCD_ERR_CUDA;
+  }
+  TTCD_CHECK_LAUNCH();
+  return TTCD_OK;
+}
+
 // CTAs that share one work unit's keys (a cluster): as many as fill the SMs
 // when the work units alone do not, at least two key tiles each.
 int pick_splits(long long units, int sms, long long key_tiles) {
@@ -2981,12 +3004,10 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   TTCD_TRY(prepare_kernel<kk>(c, smem_k, SINKB_THREADS, &kSinkBwdRegSplit));
   kq<<<static_cast<unsigned>(grid_q), SINKB_THREADS, smem_q, c.s>>>(mk, mv, a, c.st);
   TTCD_CHECK_LAUNCH();
-  kk<<<static_cast<unsigned>(grid_k), SINKB_THREADS, smem_k, c.s>>>(mq, mk, mv, mdo, a, c.st);
-  TTCD_CHECK_LAUNCH();
+  TTCD_TRY(launch_programmatic(kk, grid_k, SINKB_THREADS, smem_k, c.s, mq, mk, mv, mdo, a, c.st));
   if (p.n_far > 0) {
     const long long n = heads * 2 * n_sink * HD;
-    sink_attn_join_kernel<HD><<<static_cast<unsigned>((n + 255) / 256), 256, 0, c.s>>>(a);
-    TTCD_CHECK_LAUNCH();
+    TTCD_TRY(launch_programmatic(&sink_attn_join_kernel<HD>, (n + 255) / 256, 256, 0, c.s, a));
   }
   return TTCD_OK;
 }
@@ -3080,11 +3101,12 @@ ttcd_status ttcd_paged_kv_append(const void* qkv, void* q_out, void* k_pages, vo
   a.page_log2 = log2_of(page_size);
   a.Hq = Hq;
   a.Hkv = Hkv;
-  a.hd = hd;
   a.rotate = rope_theta > 0.f;
   a.log2_theta = a.rotate ? std::log2(static_cast<double>(rope_theta)) : 0.0;
-  const int blocks = std::min(total_q, c.sms * 8);
-  paged_append_kernel<1><<<static_cast<unsigned>(blocks), APPEND_THREADS, 0, c.s>>>(a, c.st.err);
+  // up to 16 warps per SM, each walking over tokens
+  const unsigned blocks = static_cast<unsigned>(std::min(cdiv(total_q, APPEND_WARPS), c.sms * 8));
+  auto kern = hd == 32 ? paged_append_kernel<32> : hd == 64 ? paged_append_kernel<64> : paged_append_kernel<128>;
+  kern<<<blocks, APPEND_THREADS, 0, c.s>>>(a, c.st.err);
   TTCD_CHECK_LAUNCH();
   return TTCD_OK;
 }
