@@ -8,11 +8,12 @@
 // and every K/V tile it loads serves both.  A row is (token, query head of the
 // group): a tile holds floor(128 / G) consecutive tokens of all G heads, so a
 // group of any size fills the 128 rows (G = 3: 126), and short chunks of a
-// prompt fill them with heads.  Key tiles of 128 are visited from the newest
+// prompt fill them with heads.  Where pairs of tiles would leave half of the SMs
+// idle, a CTA has tile A alone.  Key tiles of 128 are visited from the newest
 // backwards, and last the sinks' tile if the window does not reach it; a tile
 // that only one of A and B sees is computed for that one.
 //
-// SPLITS > 1 (few query tiles: a chunk of one prompt): the CTAs of a cluster take
+// splits > 1 (few query tiles and many keys: a chunk of one prompt): the CTAs of a cluster take
 // contiguous shares of the visits of one work unit and merge their partial
 // (m, l, O) through distributed shared memory, every CTA a part of the rows.
 //
@@ -47,8 +48,9 @@ struct SinkArgs {
   int max_pages, n_pages, page_log2;
   int oob_row;       // paged: first row past the pool
   int B, T;          // dense
-  int n_units;       // dense: pairs of tiles per sequence; paged: slots of them
+  int n_units;       // dense: work units per sequence; paged: slots of them
   int Hq, Hkv, G, tpt;  // tpt = 128 / G tokens per tile
+  int tpu;           // tokens per work unit: tpt or 2 tpt
   int window, n_sink;
   float scale_log2;
   int splits;        // CTAs per cluster
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
   const int rank = a.splits > 1 ? static_cast<int>(blockIdx.x) % a.splits : 0;
   const int item = static_cast<int>(blockIdx.x) / a.splits;
   const int hk = item % a.Hkv;
-  const int tpu = 2 * a.tpt;  // tokens per work unit
+  const int tpu = a.tpu;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
     return;
   }
-  const SinkVisits vis(L - n + tok0, n - tok0, a.tpt, a.window, a.n_sink);
+  const SinkVisits vis(L - n + tok0, min(n - tok0, tpu), a.tpt, a.window, a.n_sink);
   const int v0 = static_cast<int>(static_cast<long long>(vis.total) * rank / a.splits);
   const int v1 = static_cast<int>(static_cast<long long>(vis.total) * (rank + 1) / a.splits);
   // The register split of dual_window_attn_kernel: 128 x 56 + 256 x 224 = 384 x 168.

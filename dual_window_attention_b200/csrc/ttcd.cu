@@ -2751,11 +2751,13 @@ ttcd_status launch_programmatic(void (*kern)(Args...), long long grid, int threa
   return TTCD_OK;
 }
 
-// CTAs that share one work unit's keys (a cluster): as many as fill the SMs
-// when the work units alone do not, at least two key tiles each.
+// CTAs that share one work unit's keys (a cluster): as many as fill the SMs when
+// the work units alone do not, with eight key tiles each, because the merge costs
+// as much as some four visits (700 tokens, window 300, 3 key tiles: 61 us for a
+// training step with clusters of 2, 53 without).
 int pick_splits(long long units, int sms, long long key_tiles) {
   long long s = sms / std::max<long long>(units, 1);
-  s = std::min<long long>(s, key_tiles / 2);
+  s = std::min<long long>(s, key_tiles / 8);
   return static_cast<int>(std::max<long long>(1, std::min<long long>(s, 8)));
 }
 
@@ -2763,7 +2765,7 @@ template <int HD, bool PAGED>
 ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const void* v,
                             const PagedCache& pc, const Ragged& rg, void* o, float* lse, int B,
                             int T, int Hq, int Hkv, int window, int n_sink, float scale,
-                            int min_q = 1) {
+                            int min_q = 1, int max_q = 1) {
   using bf = __nv_bfloat16;
   const int G = Hq / Hkv, tpt = ATT_BM / G;
   const cuuint64_t rows = PAGED ? rg.total_q : static_cast<cuuint64_t>(B) * T;
@@ -2788,14 +2790,12 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
     a.n_pages = pc.n_pages;
     a.page_log2 = pc.page_log2;
     a.oob_row = static_cast<int>(dims[1]);
-    a.n_units = static_cast<int>(tile_slots(rg.total_q, rg.n_seq, 2 * tpt));
   } else {
     const cuuint64_t dims[4] = {hd, hkv, static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
     const cuuint64_t strides[3] = {hd * 2, hkv * hd * 2, hkv * hd * 2 * T};
     const cuuint32_t box[4] = {64, 1, ATT_BN, 1};
     if (!make_map_nd(&mk, k, 4, dims, strides, box) || !make_map_nd(&mv, v, 4, dims, strides, box))
       return TTCD_ERR_CUDA;
-    a.n_units = cdiv(T, 2 * tpt);
   }
   a.o = static_cast<bf*>(o);
   a.lse = lse;
@@ -2809,11 +2809,23 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   a.n_sink = n_sink;
   a.min_q = min_q;
   a.scale_log2 = scale * 1.4426950408889634f;
+  // Work units of `tiles` query tiles that hold work, as far as it is known here
+  // (paged: sequences of max_q new tokens).  Pairs of tiles share the loads of K and
+  // V; single ones take 2400 instead of 2900 cycles a visit, so they win where the
+  // pairs would occupy half of the SMs or less.
+  auto busy = [&](int tiles) -> long long {
+    if (!PAGED) return static_cast<long long>(cdiv(T, tiles * tpt)) * Hkv * B;
+    return Hkv * (rg.total_q / (static_cast<long long>(tiles) * tpt) +
+                  std::min(rg.n_seq, rg.total_q / max_q + 1));
+  };
+  const int tiles = 2 * busy(2) <= c.sms ? 1 : 2;
+  a.tpu = tiles * tpt;
+  a.n_units = PAGED ? static_cast<int>(tile_slots(rg.total_q, rg.n_seq, a.tpu)) : cdiv(T, a.tpu);
   const long long items = static_cast<long long>(a.n_units) * Hkv * (PAGED ? 1 : B);
   const long long keys = std::min<long long>(
-      static_cast<long long>(window) + 2 * tpt + n_sink,
+      static_cast<long long>(window) + a.tpu + n_sink,
       PAGED ? static_cast<long long>(pc.max_pages) << pc.page_log2 : T);
-  a.splits = pick_splits(items, c.sms, (keys + ATT_BN - 1) / ATT_BN);
+  a.splits = pick_splits(busy(tiles), c.sms, (keys + ATT_BN - 1) / ATT_BN);
   const long long grid = items * a.splits;
   if (grid >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
   constexpr auto kern = sink_window_attn_kernel<HD, PAGED>;
@@ -2916,7 +2928,7 @@ ttcd_status launch_paged(const Ctx& c, const void* q, const PagedCache& pc, cons
     return launch_paged_decode<HD, 16>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, false);
   const int unit = G <= 8 ? 8 / G : 16 / G;  // tokens; 0: no kernel of few rows
   TTCD_TRY((launch_sink_fwd<HD, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, pc.Hkv,
-                                      window, n_sink, scale, unit + 1)));
+                                      window, n_sink, scale, unit + 1, max_q)));
   if (unit == 0) return TTCD_OK;
   return G <= 8 ? launch_paged_decode<HD, 8>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, true)
                 : launch_paged_decode<HD, 16>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, true);
