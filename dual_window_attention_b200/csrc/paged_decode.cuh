@@ -27,6 +27,9 @@ namespace ttcd {
 
 constexpr int PDEC_WARPS = 4;
 constexpr int PDEC_THREADS = 32 * PDEC_WARPS;
+// CTAs per SM (register bound)
+template <int HD, int ROWS>
+constexpr int PDEC_CTAS = ROWS * HD <= 1024 ? (HD == 128 ? 3 : 4) : 2;
 
 struct PagedDecodeArgs {
   const __nv_bfloat16* q;  // [total_q, Hq, HD]
@@ -65,7 +68,7 @@ __device__ __forceinline__ void ld_stream(uint32_t (&r)[2], const void* p) {
 // ROWS: 8 or 16 query rows of a unit (the tensor instruction has 16 either way;
 // with 8 the registers of the others are free).
 template <int HD, int ROWS>
-__global__ void __launch_bounds__(PDEC_THREADS, ROWS * HD <= 1024 ? (HD == 128 ? 3 : 4) : 2)
+__global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS>))
     paged_decode_kernel(const PagedDecodeArgs a, uint32_t* err) {
   constexpr int NR = ROWS / 8;                  // rows per lane
   constexpr int KC = HD / 32;                   // K chunks per lane and key
@@ -86,19 +89,16 @@ __global__ void __launch_bounds__(PDEC_THREADS, ROWS * HD <= 1024 ? (HD == 128 ?
   if (blockIdx.x == 0)
     for (int s = threadIdx.x; s < a.rg.n_seq; s += PDEC_THREADS)
       if (load_span(a.rg, s, capacity).bad) atomicOr(err, DEV_ERR_BAD_INDEX);
-  // beside the tiled kernel (only_small) this grid may end only when that one has
-  auto leave = [&]() {
-    if (blockIdx.x == 0) grid_dep_wait();
-  };
+  grid_dep_launch();  // the tiled kernel of the same call may start beside the last of these
   // the first n_seq slots: the first unit of each sequence; then the further ones
   int seq = slot, tok0 = 0;
   if (slot >= a.rg.n_seq) {
     seq = find_extra_seq(a.rg, slot - a.rg.n_seq, a.tpt);
     if (seq >= 0) tok0 = extra_token(slot - a.rg.n_seq, a.rg.q_start[seq], a.tpt);
   }
-  if (seq < 0) return leave();
+  if (seq < 0) return;
   const SeqSpan sp = load_span(a.rg, seq, capacity);
-  if (tok0 >= sp.n || (a.only_small && sp.n > a.tpt)) return leave();  // the whole cluster
+  if (tok0 >= sp.n || (a.only_small && sp.n > a.tpt)) return;  // the whole cluster
   const int n_tok = min(a.tpt, sp.n - tok0), n_rows = n_tok * a.G;
   const int pos0 = sp.L - sp.n + tok0;
   const KeyRange kr = key_range(pos0, pos0 + n_tok - 1, a.window, a.n_sink);
@@ -360,7 +360,6 @@ __global__ void __launch_bounds__(PDEC_THREADS, ROWS * HD <= 1024 ? (HD == 128 ?
     __syncwarp();
     cluster_sync_all();  // nobody leaves while its part is read
   }
-  leave();
 }
 
 }  // namespace ttcd

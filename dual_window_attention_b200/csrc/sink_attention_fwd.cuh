@@ -240,9 +240,6 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* unit = reinterpret_cast<int*>(tmem_slot + 2);  // paged: sequence, first token, span
 
-  // the kernel of the short sequences may start beside the last of these CTAs
-  if (PAGED) grid_dep_launch();
-
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = a.splits > 1 ? static_cast<int>(blockIdx.x) % a.splits : 0;
@@ -313,7 +310,13 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
     q0 = seq * a.T;
     n = L = a.T;
   }
+  // after the kernel of few rows in the same call, this grid may end only when that
+  // one has
+  auto leave = [&]() {
+    if (PAGED && blockIdx.x == 0) grid_dep_wait();
+  };
   if (n == 0) {  // no tile here; the same for every CTA of the cluster
+    leave();
     if (warp == 1) tmem_dealloc(tmem, 512);
     return;
   }
@@ -624,6 +627,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       cluster_sync_all();
     }
   }
+  leave();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();

@@ -2811,21 +2811,23 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   a.scale_log2 = scale * 1.4426950408889634f;
   // Work units of `tiles` query tiles that hold work, as far as it is known here
   // (paged: sequences of max_q new tokens).  Pairs of tiles share the loads of K and
-  // V; single ones take 2400 instead of 2900 cycles a visit, so they win where the
-  // pairs would occupy half of the SMs or less.
+  // V.  Where they would leave half of the SMs idle, their keys are split over
+  // clusters if there are enough; otherwise single tiles (2400 cycles a visit instead
+  // of 2900) win.
   auto busy = [&](int tiles) -> long long {
     if (!PAGED) return static_cast<long long>(cdiv(T, tiles * tpt)) * Hkv * B;
     return Hkv * (rg.total_q / (static_cast<long long>(tiles) * tpt) +
                   std::min(rg.n_seq, rg.total_q / max_q + 1));
   };
-  const int tiles = 2 * busy(2) <= c.sms ? 1 : 2;
+  const long long key_tiles =
+      (std::min<long long>(static_cast<long long>(window) + 2 * tpt + n_sink,
+                           PAGED ? static_cast<long long>(pc.max_pages) << pc.page_log2 : T) +
+       ATT_BN - 1) / ATT_BN;
+  a.splits = pick_splits(busy(2), c.sms, key_tiles);
+  const int tiles = a.splits == 1 && 2 * busy(2) <= c.sms ? 1 : 2;
   a.tpu = tiles * tpt;
   a.n_units = PAGED ? static_cast<int>(tile_slots(rg.total_q, rg.n_seq, a.tpu)) : cdiv(T, a.tpu);
   const long long items = static_cast<long long>(a.n_units) * Hkv * (PAGED ? 1 : B);
-  const long long keys = std::min<long long>(
-      static_cast<long long>(window) + a.tpu + n_sink,
-      PAGED ? static_cast<long long>(pc.max_pages) << pc.page_log2 : T);
-  a.splits = pick_splits(busy(tiles), c.sms, (keys + ATT_BN - 1) / ATT_BN);
   const long long grid = items * a.splits;
   if (grid >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
   constexpr auto kern = sink_window_attn_kernel<HD, PAGED>;
@@ -2836,13 +2838,18 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   cfg.blockDim = dim3(ATT_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  if (a.splits > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(a.splits);
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  if (min_q > 1) {  // beside the kernel of few rows
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = a.splits > 1 ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a, c.st) != cudaSuccess) {
     cudaGetLastError();
     return TTCD_ERR_CUDA;
@@ -2851,14 +2858,15 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   return TTCD_OK;
 }
 
-// Few rows over a paged cache.  `beside`: the tiled kernel before it in the
-// stream takes the sequences of more than one unit, and this kernel may start
-// before that one has ended.
+// Few rows over a paged cache.  `beside`: the tiled kernel after it in the stream
+// takes the sequences of more than one unit.
 //
-// Clusters: CTAs for about four times what the GPU holds at once, so that the last
-// ones to run are a small part of all, while each of their warps keeps four tiles
-// of 16 keys or more.  64 sequences of 8 heads: 411, 352, 318, 348, 433 us with 1, 2,
-// 4, 8, 16 CTAs a cluster; one sequence: 119, 63, 35, 20.5, 16.4 us.
+// Clusters of `splits` CTAs per unit: as many as the GPU holds at once, or, where
+// the units alone are more, enough for four rounds, so that the last one is a small
+// part; a tile of 16 keys at least for each warp.  One wave against the next power
+// of two: 120 units of 4100 keys (head_dim 64) 26.7 and 30.8 us, 128 of 8200 (128)
+// 97 and 114, 384 of 2052 65 and 72; 512 of 8200 with 1, 2, 4, 8, 16 CTAs 411, 352,
+// 318, 348, 433.
 template <int HD, int ROWS>
 ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& pc,
                                 const Ragged& rg, void* o, float* lse, int Hq, int window,
@@ -2879,9 +2887,12 @@ ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& p
   const long long units = static_cast<long long>(rg.n_seq) * pc.Hkv;
   const long long keys = std::min<long long>(static_cast<long long>(window) + a.tpt + n_sink,
                                              static_cast<long long>(pc.max_pages) << pc.page_log2);
-  const long long want = std::min(16ll * c.sms / units, keys / (16 * 4 * PDEC_WARPS));
+  const long long held = static_cast<long long>(c.sms) * (PDEC_CTAS<HD, ROWS>);
+  const long long most = std::min(16ll, keys / (16 * PDEC_WARPS));
   a.splits = 1;
-  while (a.splits < 16 && 2 * a.splits <= want) a.splits *= 2;
+  while (2 * a.splits <= most &&
+         (units <= held ? 2 * a.splits * units <= held : a.splits * units < 4 * held))
+    a.splits *= 2;
   const long long slots =
       rg.n_seq + (beside ? 0ll : static_cast<long long>(extra_slot(rg.total_q, a.tpt)));
   const long long grid = slots * pc.Hkv * a.splits;
@@ -2892,18 +2903,13 @@ ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& p
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(PDEC_THREADS);
   cfg.stream = c.s;
-  cudaLaunchAttribute attr[2];
-  if (a.splits > 1) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(a.splits);
-    attr[cfg.numAttrs].val.clusterDim.y = 1;
-    attr[cfg.numAttrs++].val.clusterDim.z = 1;
-  }
-  if (beside) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, kern, a, c.st.err) != cudaSuccess) {
     cudaGetLastError();
     return TTCD_ERR_CUDA;
@@ -2927,11 +2933,12 @@ ttcd_status launch_paged(const Ctx& c, const void* q, const PagedCache& pc, cons
   if (G <= 16 && rows <= 16)
     return launch_paged_decode<HD, 16>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, false);
   const int unit = G <= 8 ? 8 / G : 16 / G;  // tokens; 0: no kernel of few rows
-  TTCD_TRY((launch_sink_fwd<HD, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, pc.Hkv,
-                                      window, n_sink, scale, unit + 1, max_q)));
-  if (unit == 0) return TTCD_OK;
-  return G <= 8 ? launch_paged_decode<HD, 8>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, true)
-                : launch_paged_decode<HD, 16>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, true);
+  if (unit > 0 && G <= 8)
+    TTCD_TRY((launch_paged_decode<HD, 8>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, true)));
+  if (unit > 0 && G > 8)
+    TTCD_TRY((launch_paged_decode<HD, 16>(c, q, pc, rg, o, lse, Hq, window, n_sink, scale, true)));
+  return launch_sink_fwd<HD, true>(c, q, nullptr, nullptr, pc, rg, o, lse, 0, 0, Hq, pc.Hkv, window,
+                                   n_sink, scale, unit + 1, max_q);
 }
 
 // The backward's items: query tiles, key tiles, and the query tiles past the
