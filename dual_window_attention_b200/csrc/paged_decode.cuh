@@ -13,7 +13,8 @@
 //     VE n of the keys 2p, 2p + 1, 2p + 8, 2p + 9 and pairs them by byte permutes, so
 //     that output tile i holds the columns VE n + i.  Up to 8 rows: O^T += V^T P^T.
 // The next tile's K is requested as soon as S is formed, its V after P V, and the
-// page numbers two tiles ahead: about 6 KB in flight per warp, 12 warps per SM.
+// page numbers two tiles ahead: about 6 KB in flight per warp, 12 warps per SM (or
+// 14 KB for the few warps of a small grid).
 //
 // The 4 warps of a CTA and the CTAs of a cluster share a unit's tiles and merge
 // their (m, l, O) through shared memory, then distributed shared memory.
@@ -67,8 +68,10 @@ __device__ __forceinline__ void ld_stream(uint32_t (&r)[2], const void* p) {
 
 // ROWS: 8 or 16 query rows of a unit (the tensor instruction has 16 either way;
 // with 8 the registers of the others are free).
-template <int HD, int ROWS>
-__global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS>))
+// DEPTH: tiles of K and V in registers or on their way to them (2 for grids that leave
+// an SM one or two CTAs).
+template <int HD, int ROWS, int DEPTH>
+__global__ void __launch_bounds__(PDEC_THREADS, DEPTH > 1 ? 2 : (PDEC_CTAS<HD, ROWS>))
     paged_decode_kernel(const PagedDecodeArgs a, uint32_t* err) {
   constexpr int NR = ROWS / 8;                  // rows per lane
   constexpr int KC = HD / 32;                   // K chunks per lane and key
@@ -116,8 +119,8 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS>))
     const long long r = page_row(id, a.pc.n_pages, a.pc.Hkv, hk, page);
     return r < 0 ? -1ll : (r + (key_of(v) & (page - 1))) * HD;
   };
-  uint32_t K[2][KC][4], V[4][VC][VW];
-  auto load_k = [&](long long at) {
+  uint32_t Ks[DEPTH][2][KC][4], Vs[DEPTH][4][VC][VW];
+  auto load_k = [&](long long at, uint32_t (&K)[2][KC][4]) {
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS>))
         }
       }
   };
-  auto load_v = [&](long long at) {
+  auto load_v = [&](long long at, uint32_t (&V)[4][VC][VW]) {
 #pragma unroll
     for (int y = 0; y < 4; ++y)
 #pragma unroll
@@ -143,14 +146,20 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS>))
         }
       }
   };
-  int id = page_of(v0), id1 = page_of(v0 + 1);
+  int ids[DEPTH], next_ids[DEPTH];
+#pragma unroll
+  for (int x = 0; x < DEPTH; ++x) ids[x] = page_of(v0 + x);
+#pragma unroll
+  for (int x = 0; x < DEPTH; ++x) next_ids[x] = page_of(v0 + DEPTH + x);
   bool bad = false;
-  if (v0 < v1) {
-    const long long at = row_of(v0, id);
-    bad = at < 0;
-    load_k(at);
-    load_v(at);
-  }
+#pragma unroll
+  for (int x = 0; x < DEPTH; ++x)
+    if (v0 + x < v1) {
+      const long long at = row_of(v0 + x, ids[x]);
+      bad = bad || at < 0;
+      load_k(at, Ks[x]);
+      load_v(at, Vs[x]);
+    }
   // Q in the order of K's chunks; rows that are not there are zeros
   uint32_t Q[NR][KC][4];
   int t[NR];
@@ -171,11 +180,11 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS>))
   float m[NR], l[NR];
 #pragma unroll
   for (int x = 0; x < NR; ++x) { m[x] = -INFINITY; l[x] = 0.f; }
-  for (int v = v0; v < v1; ++v) {
+  auto step = [&](int v, uint32_t (&K)[2][KC][4], uint32_t (&V)[4][VC][VW], int& next_id) {
     const int k0 = key_of(v);
-    const int id2 = page_of(v + 2);
-    const bool more = v + 1 < v1;
-    const long long next = more ? row_of(v + 1, id1) : -1;
+    const bool more = v + DEPTH < v1;
+    const long long next = more ? row_of(v + DEPTH, next_id) : -1;
+    next_id = page_of(v + 2 * DEPTH);
     bad = bad || (more && next < 0);
     float s[NR][4];  // keys 2p, 2p + 1, 2p + 8, 2p + 9
 #pragma unroll
@@ -194,7 +203,7 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS>))
         s[x][2 * nt + 1] = c[2 * x + 1];
       }
     }
-    if (more) load_k(next);
+    if (more) load_k(next, K);
     const bool all = k0 + 15 <= pos0 && (k0 > pos0 + n_tok - 1 - a.window || k0 + 16 <= a.n_sink);
     if (!all) {
 #pragma unroll
@@ -279,8 +288,12 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS>))
           mma_16816(x[0], x[1], x[2], x[3], e0, o0, e1, o1, P[0][0], P[0][1]);
         }
       }
-    if (more) load_v(next);
-    id1 = id2;
+    if (more) load_v(next, V);
+  };
+  for (int v = v0; v < v1; v += DEPTH) {
+#pragma unroll
+    for (int x = 0; x < DEPTH; ++x)
+      if (v + x < v1) step(v + x, Ks[x], Vs[x], next_ids[x]);
   }
   if (bad && lane == 0) atomicOr(err, DEV_ERR_BAD_INDEX);
   // ------------------------------------------------------------------- merge

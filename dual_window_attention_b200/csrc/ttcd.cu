@@ -2858,6 +2858,29 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   return TTCD_OK;
 }
 
+template <int HD, int ROWS, int DEPTH>
+ttcd_status launch_paged_units(const Ctx& c, const PagedDecodeArgs& a, long long grid) {
+  constexpr auto kern = paged_decode_kernel<HD, ROWS, DEPTH>;
+  TTCD_TRY(prepare_kernel<kern>(c, 0, PDEC_THREADS, nullptr, true));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(PDEC_THREADS);
+  cfg.stream = c.s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, a, c.st.err) != cudaSuccess) {
+    cudaGetLastError();
+    return TTCD_ERR_CUDA;
+  }
+  TTCD_CHECK_LAUNCH();
+  return TTCD_OK;
+}
+
 // Few rows over a paged cache.  `beside`: the tiled kernel after it in the stream
 // takes the sequences of more than one unit.
 //
@@ -2897,25 +2920,9 @@ ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& p
       rg.n_seq + (beside ? 0ll : static_cast<long long>(extra_slot(rg.total_q, a.tpt)));
   const long long grid = slots * pc.Hkv * a.splits;
   if (grid >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
-  constexpr auto kern = paged_decode_kernel<HD, ROWS>;
-  TTCD_TRY(prepare_kernel<kern>(c, 0, PDEC_THREADS, nullptr, true));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(PDEC_THREADS);
-  cfg.stream = c.s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.splits > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kern, a, c.st.err) != cudaSuccess) {
-    cudaGetLastError();
-    return TTCD_ERR_CUDA;
-  }
-  TTCD_CHECK_LAUNCH();
-  return TTCD_OK;
+  if constexpr (ROWS == 8)
+    if (grid <= 2 * c.sms) return launch_paged_units<HD, ROWS, 2>(c, a, grid);
+  return launch_paged_units<HD, ROWS, 1>(c, a, grid);
 }
 
 // The paged attention.  A sequence whose new tokens times group heads fill at
