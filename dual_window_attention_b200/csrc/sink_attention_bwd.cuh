@@ -70,8 +70,8 @@ struct SinkDqCfg {
   static constexpr int KS = 3, VS = 3;
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = KS * TILE;
-  static constexpr int DEL_OFF = V_OFF + VS * TILE;  // 2 x 128 floats
-  static constexpr int BAR_OFF = DEL_OFF + 1024;
+  static constexpr int DEL_OFF = V_OFF + VS * TILE;  // (2 + 4) x 128 floats
+  static constexpr int BAR_OFF = DEL_OFF + 3072;
   static constexpr int SMEM_RAW = 1024 + BAR_OFF + 256;
   // at least 120 KB: one CTA per SM (it takes all 512 TMEM columns)
   static constexpr int SMEM = SMEM_RAW > 122880 ? SMEM_RAW : 122880;
@@ -164,10 +164,12 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   uint64_t* s_free = s_full + 1;       // every element thread arrives
   uint64_t* dp_full = s_free + 1;
   uint64_t* ds_ready = dp_full + 1;    // every element thread arrives
-  uint64_t* done = ds_ready + 1;
+  uint64_t* sum_ready = ds_ready + 1;  // every element thread arrives
+  uint64_t* done = sum_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* del = reinterpret_cast<float*>(smem + Cfg::DEL_OFF);
+  float* sums = del + 256;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (uint64_t* p = bars; p <= done; ++p)
-      mbar_init(p, p == a_ready || p == s_free || p == ds_ready ? SINKB_ROWS : 1);
+      mbar_init(p, p == a_ready || p == s_free || p == ds_ready || p == sum_ready ? SINKB_ROWS : 1);
     *abort = 0;
     fence_mbar_init();
     tma_prefetch_map(&mapK);
@@ -337,9 +339,10 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
     const float nd = del[r] + del[128 + r];
     // a row that is not there: its P is 0
     if (qd == 0) rows[r] = split3(row_ok ? -lse * a.inv_scale : -3e38f);
-    if (qd == 1) rows[128 + r] = split3(nd);
-    const uint64_t nd2 = f2pack(nd, nd), nl2 = f2pack(nl, nl);
+    uint64_t nd2 = f2pack(nd, nd);
+    const uint64_t nl2 = f2pack(nl, nl);
     const uint32_t s_addr = tmem + lane_off + C_S + 32 * qd, dp_addr = tmem + lane_off + C_DP + 32 * qd;
+    uint64_t sum2 = f2pack(0.f, 0.f);  // of p dp
     bool ok = true;
     for (int v = 0; v < nv; ++v) {
       const int k0 = key_tile(v) * 128;
@@ -357,6 +360,23 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
       uint32_t D[16];
       float dp[32];
       tmem_ld32f(dp_addr, dp);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) sum2 = fma2(f2pack(p[c], p[c + 1]), f2pack(dp[c], dp[c + 1]), sum2);
+      if (v == nv - 1) {
+        // Now delta is known as sum_j p_j dp_j in 32 bits.  The one from dO and o carries
+        // o's rounding to bf16, an error e that all keys of a row share: it puts
+        // e sum p k into dQ, and that is a sum without cancellation over the sinks, which
+        // many queries lean on.  They are in this last visit, so it takes the better
+        // delta, and the second kernel takes it for all keys.
+        float s0, s1;
+        f2unpack(sum2, s0, s1);
+        sums[qd * 128 + r] = s0 + s1;
+        mbar_arrive(sum_ready);
+        if (!warp_wait(sum_ready, 0, st, abort)) { ok = false; break; }
+        const float exact = -((sums[r] + sums[128 + r]) + (sums[256 + r] + sums[384 + r]));
+        nd2 = f2pack(exact, exact);
+        if (qd == 0) rows[128 + r] = split3(row_ok ? exact : 0.f);
+      }
       ds32(p, dp, [&](int) { return nd2; }, D);
       tmem_st16(dp_addr, D);
       tmem_st_wait();
