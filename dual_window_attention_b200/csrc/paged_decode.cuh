@@ -13,8 +13,8 @@
 //     VE n of the keys 2p, 2p + 1, 2p + 8, 2p + 9 and pairs them by byte permutes, so
 //     that output tile i holds the columns VE n + i.  Up to 8 rows: O^T += V^T P^T.
 // The next tile's K is requested as soon as S is formed, its V after P V, and the
-// page numbers two tiles ahead: about 6 KB in flight per warp, 12 warps per SM (or
-// 14 KB for the few warps of a small grid).
+// page numbers two tiles ahead: at head_dim 128 about 6 KB in flight per warp and 12
+// warps per SM, or, with two tiles in turn, 14 KB and 8 warps.
 //
 // The 4 warps of a CTA and the CTAs of a cluster share a unit's tiles and merge
 // their (m, l, O) through shared memory, then distributed shared memory.
@@ -28,9 +28,9 @@ namespace ttcd {
 
 constexpr int PDEC_WARPS = 4;
 constexpr int PDEC_THREADS = 32 * PDEC_WARPS;
-// CTAs per SM (register bound)
-template <int HD, int ROWS>
-constexpr int PDEC_CTAS = ROWS * HD <= 1024 ? (HD == 128 ? 3 : 4) : 2;
+// CTAs per SM (register bound) of a variant.
+template <int HD, int ROWS, int DEPTH>
+constexpr int PDEC_CTAS = ROWS * HD > 1024 ? 2 : HD == 32 ? 4 : (HD == 64 ? 5 : 4) - DEPTH;
 
 struct PagedDecodeArgs {
   const __nv_bfloat16* q;  // [total_q, Hq, HD]
@@ -68,10 +68,9 @@ __device__ __forceinline__ void ld_stream(uint32_t (&r)[2], const void* p) {
 
 // ROWS: 8 or 16 query rows of a unit (the tensor instruction has 16 either way;
 // with 8 the registers of the others are free).
-// DEPTH: tiles of K and V in registers or on their way to them (2 for grids that leave
-// an SM one or two CTAs).
+// DEPTH: tiles of K and V in registers or on their way to them.
 template <int HD, int ROWS, int DEPTH>
-__global__ void __launch_bounds__(PDEC_THREADS, DEPTH > 1 ? 2 : (PDEC_CTAS<HD, ROWS>))
+__global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS, DEPTH>))
     paged_decode_kernel(const PagedDecodeArgs a, uint32_t* err) {
   constexpr int NR = ROWS / 8;                  // rows per lane
   constexpr int KC = HD / 32;                   // K chunks per lane and key

@@ -2884,12 +2884,20 @@ ttcd_status launch_paged_units(const Ctx& c, const PagedDecodeArgs& a, long long
 // Few rows over a paged cache.  `beside`: the tiled kernel after it in the stream
 // takes the sequences of more than one unit.
 //
-// Clusters of `splits` CTAs per unit: as many as the GPU holds at once, or, where
-// the units alone are more, enough for four rounds, so that the last one is a small
-// part; a tile of 16 keys at least for each warp.  One wave against the next power
-// of two: 120 units of 4100 keys (head_dim 64) 26.7 and 30.8 us, 128 of 8200 (128)
-// 97 and 114, 384 of 2052 65 and 72; 512 of 8200 with 1, 2, 4, 8, 16 CTAs 411, 352,
-// 318, 348, 433.
+// Clusters of `splits` CTAs per unit: as many as the GPU holds at once, with a tile
+// of 16 keys at least for each warp; or, where the units alone are more, enough for
+// four rounds (so that the last one is a small part) of 2048 keys each at least.
+// 120 units of 4100 keys (head_dim 64) with 2, 4, 8 CTAs: 39, 26.7, 31 us; 128 of
+// 8200 (128) 97, 114, 100; 512 of 8200 with 1, 2, 4, 8, 16: 411, 352, 318, 348, 433;
+// 800 of 2052 (64) with 1, 2, 4: 70, 82, 98.
+int pick_unit_splits(long long units, long long held, long long keys) {
+  const long long most =
+      std::min(16ll, units <= held ? keys / (16 * PDEC_WARPS) : keys / 2048);
+  int s = 1;
+  while (2 * s <= most && (units <= held ? 2 * s * units <= held : s * units < 4 * held)) s *= 2;
+  return s;
+}
+
 template <int HD, int ROWS>
 ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& pc,
                                 const Ragged& rg, void* o, float* lse, int Hq, int window,
@@ -2910,18 +2918,25 @@ ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& p
   const long long units = static_cast<long long>(rg.n_seq) * pc.Hkv;
   const long long keys = std::min<long long>(static_cast<long long>(window) + a.tpt + n_sink,
                                              static_cast<long long>(pc.max_pages) << pc.page_log2);
-  const long long held = static_cast<long long>(c.sms) * (PDEC_CTAS<HD, ROWS>);
-  const long long most = std::min(16ll, keys / (16 * PDEC_WARPS));
-  a.splits = 1;
-  while (2 * a.splits <= most &&
-         (units <= held ? 2 * a.splits * units <= held : a.splits * units < 4 * held))
-    a.splits *= 2;
+  // Two tiles in flight per warp on fewer CTAs, unless that leaves half of the warps
+  // or less: 256 units of 8200 keys 154 us instead of 174, 512 298 instead of 304,
+  // but 192 140 instead of 120 (one CTA each instead of two).
+  const long long held1 = static_cast<long long>(c.sms) * (PDEC_CTAS<HD, ROWS, 1>);
+  const int s1 = pick_unit_splits(units, held1, keys);
+  a.splits = s1;
+  bool deep = false;
+  if constexpr (ROWS == 8) {
+    const long long held2 = static_cast<long long>(c.sms) * (PDEC_CTAS<HD, ROWS, 2>);
+    const int s2 = pick_unit_splits(units, held2, keys);
+    deep = !(units <= held1 && (units > held2 || s1 >= 2 * s2));
+    if (deep) a.splits = s2;
+  }
   const long long slots =
       rg.n_seq + (beside ? 0ll : static_cast<long long>(extra_slot(rg.total_q, a.tpt)));
   const long long grid = slots * pc.Hkv * a.splits;
   if (grid >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
   if constexpr (ROWS == 8)
-    if (grid <= 2 * c.sms) return launch_paged_units<HD, ROWS, 2>(c, a, grid);
+    if (deep) return launch_paged_units<HD, ROWS, 2>(c, a, grid);
   return launch_paged_units<HD, ROWS, 1>(c, a, grid);
 }
 
