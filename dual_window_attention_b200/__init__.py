@@ -714,39 +714,58 @@ def fastweight_mlp_noalloc(u_T, u_S, beta, weights: Dict[str, torch.Tensor], p: 
     return y, state_out
 
 
-def _launching(device: torch.device, stream):
+_HERE = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launching(dev: int, stream):
     """Makes the tensors' device and the call's stream current, so that what the
     call allocates belongs to the stream that uses it."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    if stream is None:
+        return _HERE if dev == _current_device() else torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=torch.device("cuda", dev))
+    return torch.cuda.stream(stream)
 
 
-def _takes(what: str, device, **tensors) -> None:
+def _current_stream(dev: int) -> int:
+    """The handle of the device's current stream."""
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _takes(what: str, dev: int, *tensors) -> None:
     """Refuses a tensor of another shape, type or device than the call takes:
-    ``name=(tensor, shape, dtypes)``."""
-    if device.type != "cuda":
+    ``(name, tensor, shape, dtype)``."""
+    if dev < 0:
         raise ValueError(f"{what}: libttcd takes CUDA tensors only (no CPU path)")
-    for name, (t, shape, dtypes) in tensors.items():
-        if t is None or (t.get_device() == device.index and t.shape == shape and t.dtype in dtypes):
+    for name, t, shape, dtype in tensors:
+        if t is None or (t.get_device() == dev and t.shape == shape and t.dtype is dtype):
             continue
-        if t.device != device:
-            raise ValueError(f"{what}: {name} is on {t.device}, not on {device}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: {name} is on {t.device}, not on cuda:{dev}")
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        raise ValueError(f"{what}: {name} is {t.dtype}")
+        raise ValueError(f"{what}: {name} is {t.dtype}, not {dtype}")
 
 
-_F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
-_ACT = (torch.bfloat16, torch.float32)  # fp32 activations: the library says unsupported
+def _at(t) -> Optional[int]:
+    """The address of a tensor whose device is known."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("libttcd takes contiguous tensors")
+    return t.data_ptr()
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    return BF16 if t.dtype == torch.bfloat16 else F32
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def _dtype_code(what: str, t: torch.Tensor) -> int:
+    if t.dtype is _BF16:
+        return BF16
+    if t.dtype is _F32:  # the library says unsupported
+        return F32
+    raise ValueError(f"{what}: {t.dtype} activations")
 
 
 def sink_window_attn(q, k, v, window: int, n_sink: int, scale: float = 0.0, o=None,
@@ -755,19 +774,21 @@ def sink_window_attn(q, k, v, window: int, n_sink: int, scale: float = 0.0, o=No
     query at t sees key j iff j <= t and (j > t - window or j < n_sink).
     q [B, T, Hq, hd], k and v [B, T, Hkv, hd] bf16, hd 32, 64 or 128.
     Returns (o, lse [B, Hq, T] or None)."""
+    what = "sink_window_attn"
     lib = load_library()
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("sink_window_attn: q and k are [B, T, heads, head_dim]")
     B, T, Hq, hd = q.shape
     Hkv = k.shape[2]
-    _takes("sink_window_attn", q.device, q=(q, q.shape, _ACT), k=(k, (B, T, Hkv, hd), (q.dtype,)),
-           v=(v, (B, T, Hkv, hd), (q.dtype,)), o=(o, q.shape, (q.dtype,)))
-    with _launching(q.device, stream):
+    kv, dtype, dev = (B, T, Hkv, hd), q.dtype, q.get_device()
+    _takes(what, dev, ("k", k, kv, dtype), ("v", v, kv, dtype), ("o", o, q.shape, dtype))
+    code = _dtype_code(what, q)
+    with _launching(dev, stream):
         o = torch.empty_like(q) if o is None else o
-        ls = torch.empty(B, Hq, T, device=q.device, dtype=torch.float32) if lse else None
-        _check(lib.ttcd_sink_window_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(ls), B, T, Hq,
-                                         Hkv, hd, window, n_sink, scale, _dtype_code(q),
-                                         _stream(None)), "ttcd_sink_window_attn")
+        ls = torch.empty(B, Hq, T, device=q.device, dtype=_F32) if lse else None
+        _check(lib.ttcd_sink_window_attn(_at(q), _at(k), _at(v), _at(o), _at(ls), B, T, Hq, Hkv,
+                                         hd, window, n_sink, scale, code, _current_stream(dev)),
+               "ttcd_sink_window_attn")
     return o, ls
 
 
@@ -776,41 +797,45 @@ def sink_window_attn_backward(q, k, v, o, lse, d_o, window: int, n_sink: int, sc
     """Vector-Jacobian product of ``sink_window_attn`` (bf16, hd 64 or 128):
     (dq, dk, dv) in bf16 for the output gradient d_o, given the forward's o and
     lse.  Returns (dq, dk, dv, workspace)."""
+    what = "sink_window_attn_backward"
     lib = load_library()
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("sink_window_attn_backward: q and k are [B, T, heads, head_dim]")
     B, T, Hq, hd = q.shape
     Hkv = k.shape[2]
-    kv = (B, T, Hkv, hd)
-    _takes("sink_window_attn_backward", q.device, q=(q, q.shape, _BF16), k=(k, kv, _BF16),
-           v=(v, kv, _BF16), o=(o, q.shape, _BF16), lse=(lse, (B, Hq, T), _F32),
-           d_o=(d_o, q.shape, _BF16))
-    with _launching(q.device, stream):
+    kv, dev = (B, T, Hkv, hd), q.get_device()
+    _takes(what, dev, ("q", q, q.shape, _BF16), ("k", k, kv, _BF16), ("v", v, kv, _BF16),
+           ("o", o, q.shape, _BF16), ("lse", lse, (B, Hq, T), _F32), ("d_o", d_o, q.shape, _BF16))
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError(f"{what}: workspace is on {workspace.device}, not on cuda:{dev}")
+    with _launching(dev, stream):
         if workspace is None:
             need = int(lib.ttcd_sink_window_attn_backward_workspace_size(B, T, Hq, Hkv, hd, window,
                                                                          n_sink))
             workspace = alloc_workspace(need, q.device)
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         _check(lib.ttcd_sink_window_attn_backward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk),
-            _ptr(dv), B, T, Hq, Hkv, hd, window, n_sink, scale, _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(None)),
+            _at(q), _at(k), _at(v), _at(o), _at(lse), _at(d_o), _at(dq), _at(dk), _at(dv), B, T,
+            Hq, Hkv, hd, window, n_sink, scale, _at(workspace),
+            workspace.numel() * workspace.element_size(), _current_stream(dev)),
             "ttcd_sink_window_attn_backward")
     return dq, dk, dv, workspace
 
 
-def _paged(what: str, device, k_pages, v_pages, block_table, q_start, kv_len, hd: int):
+def _paged(what: str, dev: int, k_pages, v_pages, block_table, q_start, kv_len, hd: int, *more):
     """The checked sizes of a paged cache and its ragged batch: (n_seq, n_pages,
-    page_size, max_pages, Hkv)."""
+    page_size, max_pages, Hkv).  ``more``: further tensors, as ``_takes`` has them."""
     if k_pages.dim() != 4 or block_table.dim() != 2 or kv_len.dim() != 1:
         raise ValueError(f"{what}: k_pages is [n_pages, Hkv, page_size, head_dim], block_table "
                          "[n_seq, max_pages], kv_len [n_seq]")
-    n_pages, Hkv, page_size, _ = k_pages.shape
+    n_pages, Hkv, page_size, _ = pages = k_pages.shape
     n_seq, max_pages = block_table.shape
-    pages = (n_pages, Hkv, page_size, hd)
-    _takes(what, device, k_pages=(k_pages, pages, _ACT), v_pages=(v_pages, pages, (k_pages.dtype,)),
-           block_table=(block_table, (n_seq, max_pages), _I32), q_start=(q_start, (n_seq + 1,), _I32),
-           kv_len=(kv_len, (n_seq,), _I32))
+    if pages[3] != hd:
+        raise ValueError(f"{what}: k_pages has head_dim {pages[3]}, not {hd}")
+    dtype = k_pages.dtype
+    _takes(what, dev, ("k_pages", k_pages, pages, dtype), ("v_pages", v_pages, pages, dtype),
+           ("block_table", block_table, (n_seq, max_pages), _I32),
+           ("q_start", q_start, (n_seq + 1,), _I32), ("kv_len", kv_len, (n_seq,), _I32), *more)
     return n_seq, n_pages, page_size, max_pages, Hkv
 
 
@@ -822,24 +847,25 @@ def paged_kv_append(qkv, k_pages, v_pages, block_table, q_start, kv_len, n_q_hea
     and ``kv_len`` [n_seq] (with the new tokens) are int32 on the device.
     Returns the rotated q [total, Hq, hd] (``q`` when given, whose padding rows
     are left as they were)."""
+    what = "paged_kv_append"
     lib = load_library()
     if k_pages.dim() != 4 or qkv.dim() != 2:
         raise ValueError("paged_kv_append: qkv is [total, (Hq + 2 Hkv) head_dim], k_pages "
                          "[n_pages, Hkv, page_size, head_dim]")
-    hd = k_pages.shape[3]
+    _, Hkv, _, hd = k_pages.shape
+    total, dtype, dev = qkv.shape[0], k_pages.dtype, qkv.get_device()
     n_seq, n_pages, page_size, max_pages, Hkv = _paged(
-        "paged_kv_append", qkv.device, k_pages, v_pages, block_table, q_start, kv_len, hd)
-    total = qkv.shape[0]
-    _takes("paged_kv_append", qkv.device,
-           qkv=(qkv, (total, (n_q_heads + 2 * Hkv) * hd), (k_pages.dtype,)),
-           q=(q, (total, n_q_heads, hd), (qkv.dtype,)))
-    with _launching(qkv.device, stream):
+        what, dev, k_pages, v_pages, block_table, q_start, kv_len, hd,
+        ("qkv", qkv, (total, (n_q_heads + 2 * Hkv) * hd), dtype),
+        ("q", q, (total, n_q_heads, hd), dtype))
+    code = _dtype_code(what, qkv)
+    with _launching(dev, stream):
         if q is None:
-            q = torch.empty(total, n_q_heads, hd, device=qkv.device, dtype=qkv.dtype)
-        _check(lib.ttcd_paged_kv_append(_ptr(qkv), _ptr(q), _ptr(k_pages), _ptr(v_pages),
-                                        _ptr(block_table), _ptr(q_start), _ptr(kv_len), n_seq,
-                                        total, n_pages, page_size, max_pages, n_q_heads, Hkv, hd,
-                                        rope_theta, _dtype_code(qkv), _stream(None)),
+            q = torch.empty(total, n_q_heads, hd, device=qkv.device, dtype=dtype)
+        _check(lib.ttcd_paged_kv_append(_at(qkv), _at(q), _at(k_pages), _at(v_pages),
+                                        _at(block_table), _at(q_start), _at(kv_len), n_seq, total,
+                                        n_pages, page_size, max_pages, n_q_heads, Hkv, hd,
+                                        rope_theta, code, _current_stream(dev)),
                "ttcd_paged_kv_append")
     return q
 
@@ -849,27 +875,29 @@ def paged_window_attn(q, k_pages, v_pages, block_table, q_start, kv_len, window:
     """Attention of new tokens' queries q [total, Hq, hd] over a paged cache, with
     the mask of ``sink_window_attn`` at the tokens' positions; their own k and v
     are in the cache already (``paged_kv_append``).  ``max_q``: about the most new
-    tokens of any sequence (it chooses the kernel).  ``lse``: True, or a tensor
+    tokens of any sequence (it chooses the kernels).  ``lse``: True, or a tensor
     [Hq, total] to write.  Returns (o, lse or None)."""
+    what = "paged_window_attn"
     lib = load_library()
     if q.dim() != 3:
         raise ValueError("paged_window_attn: q is [total, Hq, head_dim]")
     total, Hq, hd = q.shape
-    n_seq, n_pages, page_size, max_pages, Hkv = _paged(
-        "paged_window_attn", q.device, k_pages, v_pages, block_table, q_start, kv_len, hd)
     given = lse if isinstance(lse, torch.Tensor) else None
-    _takes("paged_window_attn", q.device, q=(q, q.shape, (k_pages.dtype,)),
-           o=(o, q.shape, (q.dtype,)), lse=(given, (Hq, total), _F32))
-    with _launching(q.device, stream):
+    dtype, dev = k_pages.dtype, q.get_device()
+    n_seq, n_pages, page_size, max_pages, Hkv = _paged(
+        what, dev, k_pages, v_pages, block_table, q_start, kv_len, hd, ("q", q, q.shape, dtype),
+        ("o", o, q.shape, dtype), ("lse", given, (Hq, total), _F32))
+    code = _dtype_code(what, q)
+    with _launching(dev, stream):
         o = torch.empty_like(q) if o is None else o
         ls = given
         if ls is None and lse is True:
-            ls = torch.empty(Hq, total, device=q.device, dtype=torch.float32)
-        _check(lib.ttcd_paged_window_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
-                                          _ptr(q_start), _ptr(kv_len), _ptr(o), _ptr(ls), n_seq,
-                                          total, max_q, n_pages, page_size, max_pages, Hq, Hkv,
-                                          hd, window, n_sink, scale, _dtype_code(q),
-                                          _stream(None)), "ttcd_paged_window_attn")
+            ls = torch.empty(Hq, total, device=q.device, dtype=_F32)
+        _check(lib.ttcd_paged_window_attn(_at(q), _at(k_pages), _at(v_pages), _at(block_table),
+                                          _at(q_start), _at(kv_len), _at(o), _at(ls), n_seq, total,
+                                          max_q, n_pages, page_size, max_pages, Hq, Hkv, hd,
+                                          window, n_sink, scale, code, _current_stream(dev)),
+               "ttcd_paged_window_attn")
     return o, ls
 
 

@@ -12,10 +12,12 @@
 // product alone would be off by 0.06 radians.
 //
 // Bound by DRAM: each row is read once and written once (16 bytes per thread and
-// access).  One warp per token and no barrier of the block: lane l has the angles
-// 2l and 2l + 1 and hands them on through shared memory of its warp; then each
+// access).  One warp per token and no barrier of the block: lane l forms
+// the angles l and l + 32 and hands them on through shared memory of its warp; then each
 // lane keeps the 8 angles of its chunk for all the heads, whose loads go out four
-// at a time before the first is used.
+// at a time before the first is used.  17416 tokens of 32 heads of 128: 43.6 us, 6.5
+// TB/s (one block per token with its barriers: 94); 8 tokens: 4.1 us, a chain of
+// four loads.
 #pragma once
 #include "sink_attention.cuh"
 

@@ -19,6 +19,10 @@
 // The 4 warps of a CTA and the CTAs of a cluster share a unit's tiles and merge
 // their (m, l, O) through shared memory, then distributed shared memory.
 //
+// 64 sequences of 8200 keys, 8 heads of 128: 314 us, 6.5 TB/s (the tiled kernel 484);
+// one of them: 15 us, of which the loads of a warp's 8 tiles are half and the rest
+// the chain lengths -> page -> keys and the merge.
+//
 // Softmax as in the tiled kernel: base-2 units, the reference maximum of a row is
 // moved only when a score exceeds it by 2^8.
 #pragma once

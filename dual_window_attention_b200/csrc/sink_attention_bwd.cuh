@@ -12,13 +12,13 @@
 // A tile of queries is floor(128 / G) tokens of the G heads of one KV head, as in
 // the forward, so a group of any size fills the 128 rows and shares K and V.
 //
-// Both kernels run 384 threads: warp 0 the TMA producer, warp 1 the MMA issuer
-// (one elected lane), warps 4..11 the element work on 128 x 128 scores, thread =
-// (TMEM lane, half of the columns).  p stays in registers in 32 bits between the
-// exponential and dS.  S and dP have one buffer each, and what alternates is the
-// work: while the element warps form P from S, the tensor cores run the products
-// of dS and the next dP, and while they form dS from dP the products of P and the
-// next S.
+// Both kernels run 640 threads: warp 0 the TMA producer, warp 1 the MMA issuer
+// (one elected lane), warps 4..19 the element work on 128 x 128 scores, thread =
+// (TMEM lane, quarter of the columns).  p stays in registers in 32 bits between the
+// exponential and dS; P and dS are rounded to bf16 once, as operands of products.  S and
+// dP have one buffer each, and what alternates is the work: while the element warps
+// form P from S, the tensor cores run the products of dS and the next dP, and while
+// they form dS from dP the products of P and the next S.
 //
 // dQ kernel.  Q and dO stand in TMEM as A operands (put there by the threads of
 // their rows, which also form delta), so that shared memory is read for K and V
@@ -37,6 +37,17 @@
 // The first key tile is seen by every query through its sinks: the query tiles
 // past its window are cut into items of their own, which write fp32 partial rows of the
 // sinks, and a last kernel adds them in a fixed order.
+//
+// What bounds them, from clock marks in one CTA (cycles of a visit, 128 x 128 scores):
+//   dQ     head_dim 128: 2030, of them 1536 of products; 64: 1650, of them 1000 from S to P
+//          (the exponentials: 768 at the least), 310 of dS, the rest waits
+//   dK/dV  128: 2910 (P 1090, then dV and the next S^T 1100 and 270 of hand-overs beside
+//          dS; 2176 of products); 64: 2200 (products with 64 columns take as long as
+//          with 128: 1664)
+// 32768 tokens, 16 / 8 heads of 128, window 8192: 2.12 and 2.82 ms alone (the
+// forward 1.6); 16384, 15 / 5 of 64, window 4096: 0.43 and 0.49 ms.
+// Measured and not kept: 8 element warps 2-3 % slower; two issuing warps at head_dim
+// 128 2.41 and 3.36 ms (the products interleave and each takes twice as long).
 #pragma once
 #include "attention_bwd.cuh"
 #include "sink_attention_fwd.cuh"

@@ -13,9 +13,9 @@
 // backwards, and last the sinks' tile if the window does not reach it; a tile
 // that only one of A and B sees is computed for that one.
 //
-// splits > 1 (few query tiles and many keys: a chunk of one prompt): the CTAs of a cluster take
-// contiguous shares of the visits of one work unit and merge their partial
-// (m, l, O) through distributed shared memory, every CTA a part of the rows.
+// splits > 1 (few query tiles and many keys: a chunk of one prompt): the CTAs of a
+// cluster take contiguous shares of the visits of one work unit and merge their
+// partial (m, l, O) through distributed shared memory, every CTA a part of the rows.
 //
 // Pipeline (384 threads), TMEM (512 columns: S_A, S_B, O_A, O_B; P over its S),
 // lazy rescaling and register split are those of dual_window_attn_kernel:
@@ -30,10 +30,23 @@
 //   warp 3      checks the batch's lengths (paged, first CTA)
 //   warps 4..7  softmax of tile A (thread = row), warps 8..11 tile B
 //
-// Bound by the softmax's instruction rate per SM sub-partition, as the dual
-// kernel: one exponential pair in four on the FMA pipe, by a quartic in the
-// fractional part (relative error 2.8e-6, so that l and the log-sum-exp keep 32-bit
-// quality; the dual kernel's cubic has 1.0e-4).
+// Exponentials: one pair in four on the FMA pipe, by a quartic in the fractional part
+// (relative error 2.8e-6, so that l and the log-sum-exp keep 32-bit quality; the
+// dual kernel's cubic has 1.0e-4).
+//
+// What bounds it, from clock marks in one CTA (cycles of a visit of both tiles):
+//   head_dim 128  3270: S to P 1740 of one tile, then its 16 + 8 steps of P V and the next
+//                 Q K^T (1024, 1100-1200 with the loads' share of shared memory) and 300
+//                 of hand-overs; the tensor cores work 2048 of them
+//   head_dim 64   2860: S to P 1850 (the two tiles' softmax overlap), products and
+//                 hand-overs 1010; P V with 64 columns takes as long as with 128
+// 65536 tokens, 16 / 8 heads of 128, window 8192: 3.42 ms alone, 3.5-3.9 under the power
+// cap (2.5 ms at the measured cuBLAS rate); 16384, 15 / 5 of 64, window 4096: 0.36 ms.
+// Measured and not kept (0.37 ms as the base): two threads per row (16 softmax
+// warps) 0.44; visits of 64 or 96 keys with two score buffers and one or two issuing
+// warps 0.40-0.48; a third score buffer at head_dim 64 0.38; turns at the exponentials
+// 0.42; P in two halves 0.36 (the same), and that with the maximum beside the exponentials
+// 0.41; the share of the FMA pipe 0, 1/4, 3/8: 0.38, 0.37, 0.38.
 #pragma once
 #include "attention.cuh"
 #include "sink_attention.cuh"
@@ -569,8 +582,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       mbar_arrive(&p_full[h]);
     }
     if (ok && cnt > 0) {
-      ok = mbar_wait(&o_done[h], (cnt - 1) & 1, st, abort);
-      tc_fence_after();
+      ok = warp_wait(&o_done[h], (cnt - 1) & 1, st, abort);
     }
     auto lse_at = [&](int rw, int hd_, int tt) {
       return PAGED ? static_cast<long long>(hd_) * a.rg.total_q + rw

@@ -592,7 +592,9 @@ ttcd_status ttcd_block_decode_next_ex(const void* x_t, const float* beta_t,
  *              device, 16-byte aligned; status word first
  * Precision: bf16 tensor-core operands, fp32 sums, statistics and exponentials;
  * P (and dS in the backward) are rounded to bf16 once, as operands; o, dq, dk
- * and dv are rounded to bf16 once, at the end.  K and V (and in the backward Q
+ * and dv are rounded to bf16 once, at the end.  delta_t is sum_j p_j dp_j in fp32 for
+ * dk and for the last 128 keys of a row's walk, the sinks among them, and dO_t . o_t
+ * (with the rounded o) for the other terms of dq.  K and V (and in the backward Q
  * and d_o) are expected finite: rows that no query of a tile sees are not
  * multiplied, but a non-finite V row also reaches the queries of the same tile
  * of 128 rows whose mask hides it (their weight for it is 0).
@@ -641,7 +643,8 @@ ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const v
  *   q, o         [total_q, Hq, hd] bf16, device; o written
  *   lse          [Hq, total_q] fp32, device, nullable
  *   max_q        >= 1: about the most new tokens of any sequence; it chooses the
- *                kernel, and results hold whatever it is
+ *                kernels and their split of the keys, and results hold whatever
+ *                it is (two kernels for a batch of chunks and single tokens)
  *   Pages that no new token sees (between the sinks and the window) are never
  *   read: their table entries may hold anything.  hd 32, 64 or 128.
  * A table entry outside [0, n_pages) that is needed, or lengths that cannot be
