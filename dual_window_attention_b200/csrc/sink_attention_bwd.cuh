@@ -36,7 +36,8 @@
 // (24 bits), and the scores arrive with -lse / scale and -delta in them.
 // The first key tile is seen by every query through its sinks: the query tiles
 // past its window are cut into items of their own, which write fp32 partial rows of the
-// sinks, and a last kernel adds them in a fixed order.
+// sinks, and a last kernel adds them in a fixed order.  Where the key tiles are too few
+// for the SMs, their own queries are cut into `parts` the same way.
 //
 // What bounds them, from clock marks in one CTA (cycles of a visit, 128 x 128 scores):
 //   dQ     head_dim 128: 2030, of them 1536 of products; 64: 1650, of them 1000 from S to P
@@ -66,7 +67,11 @@ struct SinkBwdArgs {
   __nv_bfloat16* dk;         // [B, T, Hkv, HD]
   __nv_bfloat16* dv;
   uint4* rows;     // [B, Hkv, n_qt, 2, 128]: -lse / scale and -delta, three bf16 each
-  float* partial;  // [1 + n_far, B, Hkv, 2, n_sink, HD]: dk, dv of the sinks
+  // dk and dv (fp32) of a key tile's items, summed by the last kernel:
+  float* partial;    // the sinks' rows [1 + n_far, B, Hkv, 2, n_sink, HD] (the first of the
+                     // near item where parts = 1)
+  float* near_rows;  // parts > 1: [parts, B, Hkv, 2, n_kt 128, HD]
+  int parts;         // near items per key tile
   int B, T, Hq, Hkv, G, tpt, n_qt, n_kt;
   int window, n_sink;
   int n_far, far_tiles;  // items of the far queries of the sinks, query tiles each
@@ -456,12 +461,17 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   const int b = static_cast<int>(blockIdx.x) / a.Hkv % a.B;
   const int item = static_cast<int>(blockIdx.x) / (a.Hkv * a.B);
   const bool far = item < a.n_far;
-  const int kt = far ? 0 : item - a.n_far;
+  const int kt = far ? 0 : (item - a.n_far) / a.parts;
+  const int part = far ? 0 : (item - a.n_far) % a.parts;
   const int k0 = kt * 128;
   // query tiles [qt0, qt0 + nv)
-  const int qt0 = far ? a.far0 + item * a.far_tiles : k0 / a.tpt;
-  const int nv = (far ? min(qt0 + a.far_tiles, a.n_qt)
-                      : min(a.T - 1, k0 + 127 + a.window - 1) / a.tpt + 1) - qt0;
+  const int first = far ? a.far0 + item * a.far_tiles : k0 / a.tpt;
+  const int all = (far ? min(first + a.far_tiles, a.n_qt)
+                       : min(a.T - 1, k0 + 127 + a.window - 1) / a.tpt + 1) - first;
+  const int cut = far ? 0 : static_cast<int>(static_cast<long long>(all) * part / a.parts);
+  const int qt0 = first + cut;
+  // may be 0: a part without visits
+  const int nv = (far ? all : static_cast<int>(static_cast<long long>(all) * (part + 1) / a.parts)) - cut;
   const int rows_used = a.G * a.tpt;
 
   if (threadIdx.x == 0) {
@@ -579,7 +589,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         }
         __syncwarp();
       };
-      bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
+      bool ok = nv > 0 && wait(kv_full, 0) && wait(&q_full[0], 0);
       if (ok) {
         issue_s(0);
         ok = wait(&do_full[0], 0);
@@ -656,19 +666,27 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
     if (ok && warp_wait(done, 0, st, abort)) {
       const int which = qd >> 1, col = (qd & 1) * (HD / 2);
       const float f = which ? 1.f : a.scale;
-      const bool part = a.n_far > 0 && kt == 0 && r < a.n_sink;  // a sum of several items
-      const long long bh = static_cast<long long>(b) * a.Hkv + hk;
-      float* ps = a.partial + col +
-          ((((far ? item + 1 : 0) * static_cast<long long>(a.B) * a.Hkv + bh) * 2 + which) * a.n_sink + r) * HD;
+      const long long bh = static_cast<long long>(b) * a.Hkv + hk, heads = static_cast<long long>(a.B) * a.Hkv;
+      // a sum of several items goes to its partial row
+      float* ps = nullptr;
+      if (!far && a.parts > 1)
+        ps = a.near_rows + (((part * heads + bh) * 2 + which) * a.n_kt * 128 + j) * HD;
+      else if (a.n_far > 0 && kt == 0 && r < a.n_sink)
+        ps = a.partial + ((((far ? item + 1 : 0) * heads + bh) * 2 + which) * a.n_sink + r) * HD;
       __nv_bfloat16* dst = (which ? a.dv : a.dk) + ((static_cast<long long>(b) * a.T + j) * a.Hkv + hk) * HD + col;
 #pragma unroll
       for (int c = 0; c < HD / 2; c += 32) {
         float x[32];
-        tmem_ld32f(tmem + lane_off + (which ? C_DV : C_DK) + col + c, x);
+        if (nv > 0) {
+          tmem_ld32f(tmem + lane_off + (which ? C_DV : C_DK) + col + c, x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] *= f;
-        if (part && j < a.T)
-          store_f32x32(ps + c, x);
+        if (ps && j < a.T)
+          store_f32x32(ps + col + c, x);
         else if (!far && j < a.T)
           store_x32(dst + c, x);
       }
@@ -681,25 +699,38 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   }
 }
 
-// dk and dv of the sinks: the sum of the partial rows, in the items' order.
-// One thread per element; T > n_sink wherever there are far items.
+// Sums of partial rows, in the items' order: dk and dv of the sinks (parts = 1), or of
+// every key.  One thread per four elements.  Far items exist only where T > n_sink.
 template <int HD>
 __global__ void sink_attn_join_kernel(const SinkBwdArgs a) {
   grid_dep_wait();
-  const long long per = static_cast<long long>(a.B) * a.Hkv * 2 * a.n_sink * HD;
+  const int rows = a.parts > 1 ? a.T : a.n_sink;
+  const long long heads = static_cast<long long>(a.B) * a.Hkv;
   const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= per) return;
-  float x = 0.f;
-  for (int f = 0; f <= a.n_far; ++f) x += a.partial[f * per + i];
-  const int c = static_cast<int>(i % HD);
-  long long y = i / HD;
-  const int r = static_cast<int>(y % a.n_sink);
-  y /= a.n_sink;
+  if (i >= heads * 2 * rows * (HD / 4)) return;
+  const int c = static_cast<int>(i % (HD / 4)) * 4;
+  long long y = i / (HD / 4);
+  const int r = static_cast<int>(y % rows);
+  y /= rows;
   const int which = static_cast<int>(y & 1);
-  y >>= 1;
-  const int hk = static_cast<int>(y % a.Hkv);
-  const long long b = y / a.Hkv;
-  (which ? a.dv : a.dk)[((b * a.T + r) * a.Hkv + hk) * HD + c] = __float2bfloat16_rn(x);
+  const long long bh = y >> 1;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float* p) {
+    const float4 z = *reinterpret_cast<const float4*>(p);
+    x.x += z.x;
+    x.y += z.y;
+    x.z += z.z;
+    x.w += z.w;
+  };
+  if (a.parts > 1)
+    for (int f = 0; f < a.parts; ++f)
+      add(a.near_rows + (((f * heads + bh) * 2 + which) * a.n_kt * 128 + r) * HD + c);
+  if (r < a.n_sink && a.n_far > 0)
+    for (int f = a.parts > 1 ? 1 : 0; f <= a.n_far; ++f)
+      add(a.partial + (((f * heads + bh) * 2 + which) * a.n_sink + r) * HD + c);
+  const long long b = bh / a.Hkv, hk = bh % a.Hkv;
+  *reinterpret_cast<uint2*>((which ? a.dv : a.dk) + ((b * a.T + r) * a.Hkv + hk) * HD + c) =
+      make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
 }
 
 }  // namespace ttcd

@@ -2963,31 +2963,38 @@ ttcd_status launch_paged(const Ctx& c, const void* q, const PagedCache& pc, cons
                                    n_sink, scale, unit + 1, max_q);
 }
 
-// The backward's items: query tiles, key tiles, and the query tiles past the
-// window of the first key tile (far0 ...), cut into items of `far_tiles`: about as
-// long as the others (the query tiles of one window), at least 16 query tiles so
-// that an item is worth its prologue, and at most 64 partial sums.
+// The backward's items: query tiles; key tiles, each cut into `parts` of at least six
+// query tiles where there are fewer than half as many as SMs (148: another number would
+// only cut otherwise; 4000 tokens of 4 heads on one KV head 287 -> 158 us for a training
+// step; parts of four query tiles cost more than they gain); and the query tiles past the window of the first key tile (far0 ...), cut into
+// items of `far_tiles`: about as long as the others, at least 16 query tiles where there
+// is enough to do, so that an item is worth its prologue, and at most 64 partial sums.
 struct SinkBwdPlan {
-  int tpt, n_qt, n_kt, far0, far_tiles, n_far;
-  size_t rows_off, partial_off, bytes;
+  int tpt, n_qt, n_kt, parts, far0, far_tiles, n_far;
+  size_t rows_off, partial_off, near_off, bytes;
 };
 SinkBwdPlan plan_sink_bwd(int B, int T, int Hq, int Hkv, int hd, int window, int n_sink) {
   SinkBwdPlan p{};
   p.tpt = ATT_BM / (Hq / Hkv);
   p.n_qt = cdiv(T, p.tpt);
   p.n_kt = cdiv(T, 128);
+  const size_t heads = static_cast<size_t>(B) * Hkv;
+  const int visits = cdiv(std::min(window + 127, T), p.tpt);  // of a key tile
+  const long long spare = 148 / std::max<long long>(1, static_cast<long long>(heads) * p.n_kt);
+  p.parts = static_cast<int>(std::max(1ll, std::min<long long>(spare, visits / 6)));
   p.far0 = std::min(T - 1, window + 126) / p.tpt + 1;
   const int far = n_sink > 0 ? p.n_qt - p.far0 : 0;
   if (far > 0) {
-    p.far_tiles = std::max({16, cdiv(std::min(window + 127, T), p.tpt), cdiv(far, 64)});
+    p.far_tiles = std::max({p.parts > 1 ? 4 : 16, cdiv(visits, p.parts), cdiv(far, 64)});
     p.n_far = cdiv(far, p.far_tiles);
   }
-  const size_t heads = static_cast<size_t>(B) * Hkv;
   p.rows_off = kStatusBytes;
   p.partial_off = p.rows_off + heads * p.n_qt * 256 * sizeof(uint4);
-  p.bytes = p.partial_off;
+  p.near_off = p.partial_off;
   if (p.n_far > 0)
-    p.bytes += (1 + static_cast<size_t>(p.n_far)) * heads * 2 * n_sink * hd * sizeof(float);
+    p.near_off += (1 + static_cast<size_t>(p.n_far)) * heads * 2 * n_sink * hd * sizeof(float);
+  p.bytes = p.near_off;
+  if (p.parts > 1) p.bytes += p.parts * heads * 2 * p.n_kt * 128 * hd * sizeof(float);
   return p;
 }
 
@@ -3008,6 +3015,8 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   a.dv = static_cast<bf*>(dv);
   a.rows = reinterpret_cast<uint4*>(static_cast<char*>(ws) + p.rows_off);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.partial_off);
+  a.near_rows = reinterpret_cast<float*>(static_cast<char*>(ws) + p.near_off);
+  a.parts = p.parts;
   a.B = B;
   a.T = T;
   a.Hq = Hq;
@@ -3025,7 +3034,7 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   a.scale_log2 = scale * 1.4426950408889634f;
   a.inv_scale = 1.f / scale;
   const long long heads = static_cast<long long>(B) * Hkv;
-  const long long grid_q = heads * p.n_qt, grid_k = heads * (p.n_far + p.n_kt);
+  const long long grid_q = heads * p.n_qt, grid_k = heads * (p.n_far + static_cast<long long>(p.n_kt) * p.parts);
   if (grid_q >= (1ll << 31) || grid_k >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
   CUtensorMap mq, mk, mv, mdo;
   const cuuint64_t hd = HD, hq = Hq, hkv = Hkv, t = T;
@@ -3046,8 +3055,8 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   kq<<<static_cast<unsigned>(grid_q), SINKB_THREADS, smem_q, c.s>>>(mk, mv, a, c.st);
   TTCD_CHECK_LAUNCH();
   TTCD_TRY(launch_programmatic(kk, grid_k, SINKB_THREADS, smem_k, c.s, mq, mk, mv, mdo, a, c.st));
-  if (p.n_far > 0) {
-    const long long n = heads * 2 * n_sink * HD;
+  if (p.n_far > 0 || p.parts > 1) {
+    const long long n = heads * 2 * (p.parts > 1 ? T : n_sink) * (HD / 4);
     TTCD_TRY(launch_programmatic(&sink_attn_join_kernel<HD>, (n + 255) / 256, 256, 0, c.s, a));
   }
   return TTCD_OK;

@@ -150,3 +150,21 @@ def test_captured_training_step_beside_eager_ones(ttcd):
         torch.cuda.synchronize()
         for a, b, c in zip(want, out, eager):
             assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,hd,window,n_sink", [
+    (1, 1500, 4, 1, 64, 1500, 4),     # few key tiles, many queries each: cut into parts
+    (1, 1700, 6, 1, 128, 800, 128),   # and far items of a tile of sinks
+    (2, 700, 16, 1, 64, 500, 0),      # 8 tokens a tile, parts that have no visits
+])
+def test_backward_in_parts(ttcd, B, T, Hq, Hkv, hd, window, n_sink):
+    q, k, v = _inputs(B, T, Hq, Hkv, hd, seed=T)
+    d_o = make_attention_inputs(B, T, Hq, 1, hd, seed=12)[0]
+    qc, kc, vc, gc = q.cuda(), k.cuda(), v.cuda(), d_o.cuda()
+    o, lse = ttcd.sink_window_attn(qc, kc, vc, window, n_sink, lse=True)
+    got = ttcd.sink_window_attn_backward(qc, kc, vc, o, lse, gc, window, n_sink)
+    g, e = so.sink_window_attention_vjp(np64(q), np64(k), np64(v), np64(d_o), window, n_sink, hd ** -0.5)
+    for n, x in zip(("dq", "dk", "dv"), got):
+        _within(x, g[n], e[n], n)
+    again = ttcd.sink_window_attn_backward(qc, kc, vc, o, lse, gc, window, n_sink)
+    assert all(torch.equal(x, y) for x, y in zip(got[:3], again[:3]))
