@@ -15,7 +15,11 @@
 // Both kernels run 640 threads: warp 0 the TMA producer, warp 1 the MMA issuer
 // (one elected lane), warps 4..19 the element work on 128 x 128 scores, thread =
 // (TMEM lane, quarter of the columns).  p stays in registers in 32 bits between the
-// exponential and dS; P and dS are rounded to bf16 once, as operands of products.  S and
+// exponential and dS; P and dS are rounded to bf16 as operands of products.  In the sinks'
+// key tile, whose few keys carry a large part of many rows' weight, what that rounding
+// leaves is a second operand, in the columns beside the first: one visit of a row
+// in the dQ kernel, the items of the first key tile in the other.  With it the error of dq,
+// dk and dv is that of their last rounding (0.0017, relative, instead of 0.0021-0.0028).  S and
 // dP have one buffer each, and what alternates is the work: while the element warps
 // form P from S, the tensor cores run the products of dS and the next dP, and while
 // they form dS from dP the products of P and the next S.
@@ -87,7 +91,7 @@ struct SinkDqCfg {
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = KS * TILE;
   static constexpr int DEL_OFF = V_OFF + VS * TILE;  // (2 + 4) x 128 floats
-  static constexpr int BAR_OFF = DEL_OFF + 3072;
+  static constexpr int BAR_OFF = DEL_OFF + 6 * 512;
   static constexpr int SMEM_RAW = 1024 + BAR_OFF + 256;
   // at least 120 KB: one CTA per SM (it takes all 512 TMEM columns)
   static constexpr int SMEM = SMEM_RAW > 122880 ? SMEM_RAW : 122880;
@@ -153,6 +157,14 @@ __device__ __forceinline__ void ds32(const float* p, const float (&dp)[32], ND n
 #pragma unroll
   for (int i = 0; i < 32; i += 2)
     out[i >> 1] = pack2(mul2(f2pack(p[i], p[i + 1]), add2(f2pack(dp[i], dp[i + 1]), nd(i))));
+}
+
+// A pair as bf16 and what that leaves, as bf16.
+__device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  f2unpack(x, a, b);
+  hi = pack_bf16x2(a, b);
+  lo = pack_bf16x2(a - bf16lo_to_f32(hi), b - bf16hi_to_f32(hi));
 }
 
 template <int HD>
@@ -290,6 +302,12 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
           for (int kk = 0; kk < 8; ++kk)
             mma_bf16_ts_lh(tmem + C_DQ, tmem + C_DP + (kk >> 1) * 32 + (kk & 1) * 8,
                            kb + ((kk * 2048) >> 4), HI, ID_DQ, (v > 0 || kk > 0) ? 1u : 0u);
+          if (a.n_sink > 0 && v == nv - 1) {  // and what its rounding left
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts_lh(tmem + C_DQ, tmem + C_DP + (kk >> 1) * 32 + 16 + (kk & 1) * 8,
+                             kb + ((kk * 2048) >> 4), HI, ID_DQ, 1u);
+          }
           mma_commit(&k_empty[v % KS]);
         }
         __syncwarp();
@@ -393,8 +411,17 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         nd2 = f2pack(exact, exact);
         if (qd == 0) rows[128 + r] = split3(row_ok ? exact : 0.f);
       }
-      ds32(p, dp, [&](int) { return nd2; }, D);
-      tmem_st16(dp_addr, D);
+      if (a.n_sink > 0 && v == nv - 1) {  // the sinks' tile: the rest beside it
+        uint32_t D2[32];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2)
+          split2(mul2(f2pack(p[c], p[c + 1]), add2(f2pack(dp[c], dp[c + 1]), nd2)), D2[c >> 1],
+                 D2[16 + (c >> 1)]);
+        tmem_st32(dp_addr, D2);
+      } else {
+        ds32(p, dp, [&](int) { return nd2; }, D);
+        tmem_st16(dp_addr, D);
+      }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(ds_ready);
@@ -473,6 +500,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   // may be 0: a part without visits
   const int nv = (far ? all : static_cast<int>(static_cast<long long>(all) * (part + 1) / a.parts)) - cut;
   const int rows_used = a.G * a.tpt;
+  const bool split = kt == 0 && a.n_sink > 0;  // the sinks' tile
 
   if (threadIdx.x == 0) {
     for (uint64_t* p = bars; p <= done; ++p) mbar_init(p, (p >= p_ready && p < dp_full) || p == ds_ready ? SINKB_ROWS : 1);
@@ -585,6 +613,12 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
           for (int kk = 0; kk < 8; ++kk)
             mma_bf16_ts_lh(tmem + d, tmem + at + (kk >> 1) * 32 + (kk & 1) * 8,
                            b_mn + ((kk * 2048) >> 4), HI, ID_KV, (!first || kk > 0) ? 1u : 0u);
+          if (split) {  // and what its rounding left
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts_lh(tmem + d, tmem + at + (kk >> 1) * 32 + 16 + (kk & 1) * 8,
+                             b_mn + ((kk * 2048) >> 4), HI, ID_KV, 1u);
+          }
           mma_commit(bar);
         }
         __syncwarp();
@@ -645,19 +679,32 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         mask_scores(p, [&](int) { return low_bits(hi) & ~low_bits(lo); });
       }
       probs32(p, a.scale_log2, [](int) { return 0ull; });
-      uint32_t P[16];
+      uint32_t P[32];
+      if (split) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) P[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
-      tmem_st16(s_at, P);
+        for (int c = 0; c < 32; c += 2) split2(f2pack(p[c], p[c + 1]), P[c >> 1], P[16 + (c >> 1)]);
+        tmem_st32(s_at, P);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) P[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
+        tmem_st16(s_at, *reinterpret_cast<uint32_t(*)[16]>(&P[0]));
+      }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&p_ready[v % NBS]);
       if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
       float dp[32];
       tmem_ld32f(dp_addr, dp);
+      if (split) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) P[c >> 1] = pack2(mul2(f2pack(p[c], p[c + 1]), f2pack(dp[c], dp[c + 1])));
-      tmem_st16(dp_addr, P);
+        for (int c = 0; c < 32; c += 2)
+          split2(mul2(f2pack(p[c], p[c + 1]), f2pack(dp[c], dp[c + 1])), P[c >> 1], P[16 + (c >> 1)]);
+        tmem_st32(dp_addr, P);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) P[c >> 1] = pack2(mul2(f2pack(p[c], p[c + 1]), f2pack(dp[c], dp[c + 1])));
+        tmem_st16(dp_addr, *reinterpret_cast<uint32_t(*)[16]>(&P[0]));
+      }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(ds_ready);

@@ -2886,7 +2886,7 @@ ttcd_status launch_paged_units(const Ctx& c, const PagedDecodeArgs& a, long long
 //
 // Clusters of `splits` CTAs per unit: as many as the GPU holds at once, with a tile
 // of 16 keys at least for each warp; or, where the units alone are more, enough for
-// four rounds (so that the last one is a small part) of 2048 keys each at least.
+// four waves (so that the last one is a small part) of 2048 keys each at least.
 // 120 units of 4100 keys (head_dim 64) with 2, 4, 8 CTAs: 39, 26.7, 31 us; 128 of
 // 8200 (128) 97, 114, 100; 512 of 8200 with 1, 2, 4, 8, 16: 411, 352, 318, 348, 433;
 // 800 of 2052 (64) with 1, 2, 4: 70, 82, 98.
