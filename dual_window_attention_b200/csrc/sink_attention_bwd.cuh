@@ -72,10 +72,11 @@ struct SinkBwdArgs {
   __nv_bfloat16* dv;
   uint4* rows;     // [B, Hkv, n_qt, 2, 128]: -lse / scale and -delta, three bf16 each
   // dk and dv (fp32) of a key tile's items, summed by the last kernel:
-  float* partial;    // the sinks' rows [1 + n_far, B, Hkv, 2, n_sink, HD] (the first of the
-                     // near item where parts = 1)
+  float* partial;    // the sinks' rows [n_far + 1, B, Hkv, 2, n_sink, HD]; the last are those of
+                     // the first tile's near item where it is one (parts0 = 1)
+  float* near0;      // parts0 > 1: [parts0, B, Hkv, 2, 128, HD]
   float* near_rows;  // parts > 1: [parts, B, Hkv, 2, n_kt 128, HD]
-  int parts;         // near items per key tile
+  int parts0, parts;  // near items of the first key tile, of each other one
   int B, T, Hq, Hkv, G, tpt, n_qt, n_kt;
   int window, n_sink;
   int n_far, far_tiles;  // items of the far queries of the sinks, query tiles each
@@ -151,20 +152,31 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// dS of 32 columns: p (dp + nd), packed bf16 pairs.
-template <class ND>
-__device__ __forceinline__ void ds32(const float* p, const float (&dp)[32], ND nd, uint32_t* out) {
+// dS of 32 columns, p (dp + nd), in place of dp.
+__device__ __forceinline__ void ds32(const float (&p)[32], float (&dp)[32], uint64_t nd2) {
 #pragma unroll
   for (int i = 0; i < 32; i += 2)
-    out[i >> 1] = pack2(mul2(f2pack(p[i], p[i + 1]), add2(f2pack(dp[i], dp[i + 1]), nd(i))));
+    f2unpack(mul2(f2pack(p[i], p[i + 1]), add2(f2pack(dp[i], dp[i + 1]), nd2)), dp[i], dp[i + 1]);
 }
 
-// A pair as bf16 and what that leaves, as bf16.
-__device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
-  float a, b;
-  f2unpack(x, a, b);
-  hi = pack_bf16x2(a, b);
-  lo = pack_bf16x2(a - bf16lo_to_f32(hi), b - bf16hi_to_f32(hi));
+// What the rounding of a pair to `hi` leaves, as bf16.
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
+  return pack_bf16x2(a - bf16lo_to_f32(hi), b - bf16hi_to_f32(hi));
+}
+// 32 columns as bf16 over the first half of their own columns, and, where `split`,
+// what that leaves over the second half.
+__device__ __forceinline__ void store_operand(uint32_t taddr, const float (&x)[32], bool split) {
+  uint32_t w[16];
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) w[c >> 1] = pack_bf16x2(x[c], x[c + 1]);
+  tmem_st16(taddr, w);
+  if (split) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) w[c >> 1] = rest2(x[c], x[c + 1], w[c >> 1]);
+    tmem_st16(taddr + 16, w);
+  }
+  tmem_st_wait();
+  tc_fence_before();
 }
 
 template <int HD>
@@ -391,7 +403,6 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         mask_scores(p, [&](int) { return seen_bits(t, k0 + 32 * qd, a.window, a.n_sink); });
       probs32(p, a.scale_log2, [&](int) { return nl2; });
       if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
-      uint32_t D[16];
       float dp[32];
       tmem_ld32f(dp_addr, dp);
 #pragma unroll
@@ -411,19 +422,8 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         nd2 = f2pack(exact, exact);
         if (qd == 0) rows[128 + r] = split3(row_ok ? exact : 0.f);
       }
-      if (a.n_sink > 0 && v == nv - 1) {  // the sinks' tile: the rest beside it
-        uint32_t D2[32];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2)
-          split2(mul2(f2pack(p[c], p[c + 1]), add2(f2pack(dp[c], dp[c + 1]), nd2)), D2[c >> 1],
-                 D2[16 + (c >> 1)]);
-        tmem_st32(dp_addr, D2);
-      } else {
-        ds32(p, dp, [&](int) { return nd2; }, D);
-        tmem_st16(dp_addr, D);
-      }
-      tmem_st_wait();
-      tc_fence_before();
+      ds32(p, dp, nd2);
+      store_operand(dp_addr, dp, a.n_sink > 0 && v == nv - 1);
       mbar_arrive(ds_ready);
     }
     if (ok && warp_wait(done, 0, st, abort)) {
@@ -488,17 +488,19 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   const int b = static_cast<int>(blockIdx.x) / a.Hkv % a.B;
   const int item = static_cast<int>(blockIdx.x) / (a.Hkv * a.B);
   const bool far = item < a.n_far;
-  const int kt = far ? 0 : (item - a.n_far) / a.parts;
-  const int part = far ? 0 : (item - a.n_far) % a.parts;
+  const int near = item - a.n_far, other = near - a.parts0;
+  const int kt = other < 0 ? 0 : 1 + other / a.parts;
+  const int parts = other < 0 ? a.parts0 : a.parts;
+  const int part = far ? 0 : other < 0 ? near : other % a.parts;
   const int k0 = kt * 128;
   // query tiles [qt0, qt0 + nv)
   const int first = far ? a.far0 + item * a.far_tiles : k0 / a.tpt;
   const int all = (far ? min(first + a.far_tiles, a.n_qt)
                        : min(a.T - 1, k0 + 127 + a.window - 1) / a.tpt + 1) - first;
-  const int cut = far ? 0 : static_cast<int>(static_cast<long long>(all) * part / a.parts);
+  const int cut = far ? 0 : static_cast<int>(static_cast<long long>(all) * part / parts);
   const int qt0 = first + cut;
   // may be 0: a part without visits
-  const int nv = (far ? all : static_cast<int>(static_cast<long long>(all) * (part + 1) / a.parts)) - cut;
+  const int nv = (far ? all : static_cast<int>(static_cast<long long>(all) * (part + 1) / parts)) - cut;
   const int rows_used = a.G * a.tpt;
   const bool split = kt == 0 && a.n_sink > 0;  // the sinks' tile
 
@@ -679,34 +681,15 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         mask_scores(p, [&](int) { return low_bits(hi) & ~low_bits(lo); });
       }
       probs32(p, a.scale_log2, [](int) { return 0ull; });
-      uint32_t P[32];
-      if (split) {
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) split2(f2pack(p[c], p[c + 1]), P[c >> 1], P[16 + (c >> 1)]);
-        tmem_st32(s_at, P);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) P[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
-        tmem_st16(s_at, *reinterpret_cast<uint32_t(*)[16]>(&P[0]));
-      }
-      tmem_st_wait();
-      tc_fence_before();
+      store_operand(s_at, p, split);
       mbar_arrive(&p_ready[v % NBS]);
       if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
       float dp[32];
       tmem_ld32f(dp_addr, dp);
-      if (split) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 2)
-          split2(mul2(f2pack(p[c], p[c + 1]), f2pack(dp[c], dp[c + 1])), P[c >> 1], P[16 + (c >> 1)]);
-        tmem_st32(dp_addr, P);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) P[c >> 1] = pack2(mul2(f2pack(p[c], p[c + 1]), f2pack(dp[c], dp[c + 1])));
-        tmem_st16(dp_addr, *reinterpret_cast<uint32_t(*)[16]>(&P[0]));
-      }
-      tmem_st_wait();
-      tc_fence_before();
+      for (int c = 0; c < 32; c += 2)
+        f2unpack(mul2(f2pack(p[c], p[c + 1]), f2pack(dp[c], dp[c + 1])), dp[c], dp[c + 1]);
+      store_operand(dp_addr, dp, split);
       mbar_arrive(ds_ready);
     }
     // ------------------------------------ halves of the dK (quarters 0, 1) and dV rows
@@ -716,10 +699,11 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
       const long long bh = static_cast<long long>(b) * a.Hkv + hk, heads = static_cast<long long>(a.B) * a.Hkv;
       // a sum of several items goes to its partial row
       float* ps = nullptr;
-      if (!far && a.parts > 1)
-        ps = a.near_rows + (((part * heads + bh) * 2 + which) * a.n_kt * 128 + j) * HD;
+      if (!far && parts > 1)
+        ps = kt == 0 ? a.near0 + (((part * heads + bh) * 2 + which) * 128 + r) * HD
+                     : a.near_rows + (((part * heads + bh) * 2 + which) * a.n_kt * 128 + j) * HD;
       else if (a.n_far > 0 && kt == 0 && r < a.n_sink)
-        ps = a.partial + ((((far ? item + 1 : 0) * heads + bh) * 2 + which) * a.n_sink + r) * HD;
+        ps = a.partial + ((((far ? item : a.n_far) * heads + bh) * 2 + which) * a.n_sink + r) * HD;
       __nv_bfloat16* dst = (which ? a.dv : a.dk) + ((static_cast<long long>(b) * a.T + j) * a.Hkv + hk) * HD + col;
 #pragma unroll
       for (int c = 0; c < HD / 2; c += 32) {
@@ -746,12 +730,15 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   }
 }
 
-// Sums of partial rows, in the items' order: dk and dv of the sinks (parts = 1), or of
-// every key.  One thread per four elements.  Far items exist only where T > n_sink.
+// Sums of partial rows, in the items' order: dk and dv of the sinks, of the first key
+// tile (parts0 > 1) or of every key (parts > 1).  One thread per four elements.
+__host__ __device__ __forceinline__ int join_rows(const SinkBwdArgs& a) {
+  return a.parts > 1 ? a.T : a.parts0 > 1 ? (a.T < 128 ? a.T : 128) : a.n_sink;
+}
 template <int HD>
 __global__ void sink_attn_join_kernel(const SinkBwdArgs a) {
   grid_dep_wait();
-  const int rows = a.parts > 1 ? a.T : a.n_sink;
+  const int rows = join_rows(a);
   const long long heads = static_cast<long long>(a.B) * a.Hkv;
   const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= heads * 2 * rows * (HD / 4)) return;
@@ -769,11 +756,15 @@ __global__ void sink_attn_join_kernel(const SinkBwdArgs a) {
     x.z += z.z;
     x.w += z.w;
   };
-  if (a.parts > 1)
+  if (r >= 128) {
     for (int f = 0; f < a.parts; ++f)
       add(a.near_rows + (((f * heads + bh) * 2 + which) * a.n_kt * 128 + r) * HD + c);
+  } else if (a.parts0 > 1) {
+    for (int f = 0; f < a.parts0; ++f)
+      add(a.near0 + (((f * heads + bh) * 2 + which) * 128 + r) * HD + c);
+  }
   if (r < a.n_sink && a.n_far > 0)
-    for (int f = a.parts > 1 ? 1 : 0; f <= a.n_far; ++f)
+    for (int f = 0; f < a.n_far + (a.parts0 > 1 ? 0 : 1); ++f)
       add(a.partial + (((f * heads + bh) * 2 + which) * a.n_sink + r) * HD + c);
   const long long b = bh / a.Hkv, hk = bh % a.Hkv;
   *reinterpret_cast<uint2*>((which ? a.dv : a.dk) + ((b * a.T + r) * a.Hkv + hk) * HD + c) =

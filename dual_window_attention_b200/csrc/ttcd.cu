@@ -2970,8 +2970,8 @@ ttcd_status launch_paged(const Ctx& c, const void* q, const PagedCache& pc, cons
 // items of `far_tiles`: about as long as the others, at least 16 query tiles where there
 // is enough to do, so that an item is worth its prologue, and at most 64 partial sums.
 struct SinkBwdPlan {
-  int tpt, n_qt, n_kt, parts, far0, far_tiles, n_far;
-  size_t rows_off, partial_off, near_off, bytes;
+  int tpt, n_qt, n_kt, parts0, parts, far0, far_tiles, n_far;
+  size_t rows_off, partial_off, near0_off, near_off, bytes;
 };
 SinkBwdPlan plan_sink_bwd(int B, int T, int Hq, int Hkv, int hd, int window, int n_sink) {
   SinkBwdPlan p{};
@@ -2982,19 +2982,22 @@ SinkBwdPlan plan_sink_bwd(int B, int T, int Hq, int Hkv, int hd, int window, int
   const int visits = cdiv(std::min(window + 127, T), p.tpt);  // of a key tile
   const long long spare = 148 / std::max<long long>(1, static_cast<long long>(heads) * p.n_kt);
   p.parts = static_cast<int>(std::max(1ll, std::min<long long>(spare, visits / 6)));
+  // The first key tile's visits take half as long again (its P and dS are two operands
+  // each): in a grid of a wave or two it would end last.
+  const bool long0 = n_sink > 0 && visits >= 12 && heads * p.n_kt < 2 * 148;
+  p.parts0 = long0 ? 2 * p.parts : p.parts;
   p.far0 = std::min(T - 1, window + 126) / p.tpt + 1;
   const int far = n_sink > 0 ? p.n_qt - p.far0 : 0;
   if (far > 0) {
-    p.far_tiles = std::max({p.parts > 1 ? 4 : 16, cdiv(visits, p.parts), cdiv(far, 64)});
+    p.far_tiles = std::max({p.parts > 1 ? 4 : 16, cdiv(visits, p.parts0), cdiv(far, 64)});
     p.n_far = cdiv(far, p.far_tiles);
   }
   p.rows_off = kStatusBytes;
   p.partial_off = p.rows_off + heads * p.n_qt * 256 * sizeof(uint4);
-  p.near_off = p.partial_off;
-  if (p.n_far > 0)
-    p.near_off += (1 + static_cast<size_t>(p.n_far)) * heads * 2 * n_sink * hd * sizeof(float);
-  p.bytes = p.near_off;
-  if (p.parts > 1) p.bytes += p.parts * heads * 2 * p.n_kt * 128 * hd * sizeof(float);
+  const size_t row = heads * 2 * hd * sizeof(float);  // a row of dk and dv of every head
+  p.near0_off = p.partial_off + (p.n_far > 0 ? (1 + static_cast<size_t>(p.n_far)) * n_sink * row : 0);
+  p.near_off = p.near0_off + (p.parts0 > 1 ? p.parts0 * row * 128 : 0);
+  p.bytes = p.near_off + (p.parts > 1 ? p.parts * row * p.n_kt * 128 : 0);
   return p;
 }
 
@@ -3016,6 +3019,8 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   a.rows = reinterpret_cast<uint4*>(static_cast<char*>(ws) + p.rows_off);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.partial_off);
   a.near_rows = reinterpret_cast<float*>(static_cast<char*>(ws) + p.near_off);
+  a.near0 = reinterpret_cast<float*>(static_cast<char*>(ws) + p.near0_off);
+  a.parts0 = p.parts0;
   a.parts = p.parts;
   a.B = B;
   a.T = T;
@@ -3034,7 +3039,7 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   a.scale_log2 = scale * 1.4426950408889634f;
   a.inv_scale = 1.f / scale;
   const long long heads = static_cast<long long>(B) * Hkv;
-  const long long grid_q = heads * p.n_qt, grid_k = heads * (p.n_far + static_cast<long long>(p.n_kt) * p.parts);
+  const long long grid_q = heads * p.n_qt, grid_k = heads * (p.n_far + p.parts0 + (p.n_kt - 1ll) * p.parts);
   if (grid_q >= (1ll << 31) || grid_k >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
   CUtensorMap mq, mk, mv, mdo;
   const cuuint64_t hd = HD, hq = Hq, hkv = Hkv, t = T;
@@ -3055,8 +3060,8 @@ ttcd_status launch_sink_bwd(const Ctx& c, const void* q, const void* k, const vo
   kq<<<static_cast<unsigned>(grid_q), SINKB_THREADS, smem_q, c.s>>>(mk, mv, a, c.st);
   TTCD_CHECK_LAUNCH();
   TTCD_TRY(launch_programmatic(kk, grid_k, SINKB_THREADS, smem_k, c.s, mq, mk, mv, mdo, a, c.st));
-  if (p.n_far > 0 || p.parts > 1) {
-    const long long n = heads * 2 * (p.parts > 1 ? T : n_sink) * (HD / 4);
+  if (p.n_far > 0 || p.parts0 > 1) {
+    const long long n = heads * 2 * join_rows(a) * (HD / 4);
     TTCD_TRY(launch_programmatic(&sink_attn_join_kernel<HD>, (n + 255) / 256, 256, 0, c.s, a));
   }
   return TTCD_OK;
