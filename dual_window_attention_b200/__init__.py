@@ -723,6 +723,9 @@ def _launching(dev: int, stream):
     call allocates belongs to the stream that uses it."""
     if stream is None:
         return _HERE if dev == _current_device() else torch.cuda.device(dev)
+    at = getattr(stream, "device", None)
+    if at is not None and at.index != dev:
+        raise ValueError(f"libttcd: the stream is on {at}, the tensors on cuda:{dev}")
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream), device=torch.device("cuda", dev))
     return torch.cuda.stream(stream)
@@ -760,6 +763,18 @@ def _at(t) -> Optional[int]:
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 
 
+def _c_int(what: str, name: str, x: int) -> int:
+    """A number that a C int holds (ctypes would cut off its upper bits)."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{what}: {name} {x} is no 32-bit number")
+    return x
+
+
+def _window(what: str, x: int) -> int:
+    """A window as a C int: one beyond every position hides nothing, like 2^30."""
+    return _c_int(what, "window", x if x < 1 << 30 else 1 << 30)
+
+
 def _dtype_code(what: str, t: torch.Tensor) -> int:
     if t.dtype is _BF16:
         return BF16
@@ -778,6 +793,7 @@ def sink_window_attn(q, k, v, window: int, n_sink: int, scale: float = 0.0, o=No
     lib = load_library()
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("sink_window_attn: q and k are [B, T, heads, head_dim]")
+    window, n_sink = _window(what, window), _c_int(what, "n_sink", n_sink)
     B, T, Hq, hd = q.shape
     Hkv = k.shape[2]
     kv, dtype, dev = (B, T, Hkv, hd), q.dtype, q.get_device()
@@ -801,6 +817,7 @@ def sink_window_attn_backward(q, k, v, o, lse, d_o, window: int, n_sink: int, sc
     lib = load_library()
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("sink_window_attn_backward: q and k are [B, T, heads, head_dim]")
+    window, n_sink = _window(what, window), _c_int(what, "n_sink", n_sink)
     B, T, Hq, hd = q.shape
     Hkv = k.shape[2]
     kv, dev = (B, T, Hkv, hd), q.get_device()
@@ -881,6 +898,8 @@ def paged_window_attn(q, k_pages, v_pages, block_table, q_start, kv_len, window:
     lib = load_library()
     if q.dim() != 3:
         raise ValueError("paged_window_attn: q is [total, Hq, head_dim]")
+    window, n_sink = _window(what, window), _c_int(what, "n_sink", n_sink)
+    max_q = _c_int(what, "max_q", max_q)
     total, Hq, hd = q.shape
     given = lse if isinstance(lse, torch.Tensor) else None
     dtype, dev = k_pages.dtype, q.get_device()

@@ -168,3 +168,14 @@ def test_backward_in_parts(ttcd, B, T, Hq, Hkv, hd, window, n_sink):
         _within(x, g[n], e[n], n)
     again = ttcd.sink_window_attn_backward(qc, kc, vc, o, lse, gc, window, n_sink)
     assert all(torch.equal(x, y) for x, y in zip(got[:3], again[:3]))
+
+
+@pytest.mark.parametrize("window", [1 << 30, 1 << 31, (1 << 32) + 7, 1 << 62])
+def test_a_window_of_any_length_is_causal(ttcd, window):
+    q, k, v = (x.cuda() for x in make_attention_inputs(1, 300, 4, 2, 64, seed=8))
+    o, lse = ttcd.sink_window_attn(q, k, v, 300, 4, lse=True)
+    wide, wide_lse = ttcd.sink_window_attn(q, k, v, window, 4, lse=True)
+    assert torch.equal(o, wide) and torch.equal(lse, wide_lse)
+    want = ttcd.sink_window_attn_backward(q, k, v, o, lse, q, 300, 4)
+    got = ttcd.sink_window_attn_backward(q, k, v, o, lse, q, window, 4)
+    assert all(torch.equal(a, b) for a, b in zip(want[:3], got[:3]))

@@ -129,3 +129,32 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
     with pytest.raises(ValueError):
         ttcd.paged_kv_append(torch.zeros(9, 8 * 64, dtype=torch.bfloat16), pages, pages, i[None],
                              torch.zeros(2, dtype=torch.int32), i, 4)
+
+
+WIDE = [1 << 31, (1 << 32) + 1, -(1 << 32) + 1]
+
+
+@pytest.mark.parametrize("x", WIDE)
+def test_binding_does_not_cut_numbers_to_32_bits(lib, x):
+    q, kv = torch.zeros(1, 9, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 9, 2, 64, dtype=torch.bfloat16)
+    pages, i = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    paged = (q[0], pages, pages, i[None], torch.zeros(2, dtype=torch.int32), i)
+    lse = torch.zeros(1, 4, 9)
+    windows = [x] if x < 0 else []  # a long window is one that hides nothing
+    for w, s in [(4, x)] + [(w, 1) for w in windows]:
+        name = "n_sink" if s == x else "window"
+        with pytest.raises(ValueError, match=name):
+            ttcd.sink_window_attn(q, kv, kv, w, s)
+        with pytest.raises(ValueError, match=name):
+            ttcd.sink_window_attn_backward(q, kv, kv, q, lse, q, w, s)
+        with pytest.raises(ValueError, match=name):
+            ttcd.paged_window_attn(*paged, w, s, 9)
+    with pytest.raises(ValueError, match="max_q"):
+        ttcd.paged_window_attn(*paged, 4, 1, x)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 5
+    with pytest.raises(ValueError, match="cuda:1"):
+        ttcd._launching(0, Stream())
