@@ -24,7 +24,12 @@
 // the chain lengths -> page -> keys and the merge.
 //
 // Softmax as in the tiled kernel: base-2 units, the reference maximum of a row is
-// moved only when a score exceeds it by 2^8.
+// moved only when a score exceeds it by 2^8.  P becomes a bf16 operand, and the rounding
+// of a key with most of a row's weight (a sink often has it) would show in the result,
+// up to 2^-8 of it, with few rows to average over.  head_dim 128: a warp scales its O by
+// sum p / sum round(p), in which the rounding of such a key falls out (registers are
+// short: what the rounding leaves as a second operand costs 13 % there).  Up to 64: that
+// second operand, at no cost (the scaling 10 %).  lse is that of the unrounded p.
 #pragma once
 #include "sink_attention_fwd.cuh"
 
@@ -81,6 +86,7 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS, DEPTH>))
   constexpr int VE = HD >= 64 ? 8 : HD / 8;     // V elements per load
   constexpr int VC = HD / (8 * VE);             // V chunks per lane and key
   constexpr int VW = VE / 2;                    // words of a V chunk
+  constexpr bool REST = HD <= 64;               // P as two operands
   __shared__ float part[PDEC_WARPS][ROWS][HD + 4];
   __shared__ float2 ml[PDEC_WARPS][ROWS];       // reference maximum, sum
   __shared__ float2 ml_cta[ROWS];
@@ -180,9 +186,26 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS, DEPTH>))
   }
   // 16 rows: [column 2p + e of output tile i][row n + 8 x]; 8 rows: see below
   float O[VC][NR * VE / 2][4] = {};
-  float m[NR], l[NR];
+  float m[NR], l[NR], lr[NR];  // reference maximum, sum of p, of p as rounded
 #pragma unroll
-  for (int x = 0; x < NR; ++x) { m[x] = -INFINITY; l[x] = 0.f; }
+  for (int x = 0; x < NR; ++x) { m[x] = -INFINITY; l[x] = lr[x] = 0.f; }
+  // O times a factor of each row n + 8 x
+  auto scale_rows = [&](const float (&f)[NR]) {
+    float g[4];
+    if (NR > 1) {
+      g[0] = g[1] = f[0];
+      g[2] = g[3] = f[NR - 1];
+    } else {  // rows 2p and 2p + 1
+      g[0] = g[2] = __shfl_sync(0xffffffffu, f[0], 8 * p);
+      g[1] = g[3] = __shfl_sync(0xffffffffu, f[0], 8 * p + 4);
+    }
+#pragma unroll
+    for (int c = 0; c < VC; ++c)
+#pragma unroll
+      for (int i = 0; i < NR * VE / 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[c][i][e] *= g[e];
+  };
   auto step = [&](int v, uint32_t (&K)[2][KC][4], uint32_t (&V)[4][VC][VW], int& next_id) {
     const int k0 = key_of(v);
     const bool more = v + DEPTH < v1;
@@ -242,25 +265,13 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS, DEPTH>))
           const float al = ex2_approx(m[x] - g);
           m[x] = g;
           l[x] *= al;
+          lr[x] *= al;
           f[x] = al;
         }
       }
-      float g[4];  // factor of each accumulator of a quad
-      if (NR > 1) {
-        g[0] = g[1] = f[0];
-        g[2] = g[3] = f[NR - 1];
-      } else {  // rows 2p and 2p + 1
-        g[0] = g[2] = __shfl_sync(0xffffffffu, f[0], 8 * p);
-        g[1] = g[3] = __shfl_sync(0xffffffffu, f[0], 8 * p + 4);
-      }
-#pragma unroll
-      for (int c = 0; c < VC; ++c)
-#pragma unroll
-        for (int i = 0; i < NR * VE / 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) O[c][i][e] *= g[e];
+      scale_rows(f);
     }
-    uint32_t P[NR][2];
+    uint32_t P[NR][2], R[NR][2];  // P, and (REST) what its rounding leaves
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const float nm = m[x] == -INFINITY ? 0.f : -m[x];
@@ -270,6 +281,13 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS, DEPTH>))
       l[x] += (e[0] + e[1]) + (e[2] + e[3]);
       P[x][0] = pack_bf16x2(e[0], e[1]);
       P[x][1] = pack_bf16x2(e[2], e[3]);
+      if constexpr (REST) {
+        R[x][0] = rest2(e[0], e[1], P[x][0]);
+        R[x][1] = rest2(e[2], e[3], P[x][1]);
+      } else {
+        lr[x] += (bf16lo_to_f32(P[x][0]) + bf16hi_to_f32(P[x][0])) +
+                 (bf16lo_to_f32(P[x][1]) + bf16hi_to_f32(P[x][1]));
+      }
     }
 #pragma unroll
     for (int c = 0; c < VC; ++c)
@@ -284,11 +302,16 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS, DEPTH>))
           float(&x)[4] = O[c][2 * w], (&y)[4] = O[c][2 * w + 1];
           mma_16816(x[0], x[1], x[2], x[3], P[0][0], P[1][0], P[0][1], P[1][1], e0, e1);
           mma_16816(y[0], y[1], y[2], y[3], P[0][0], P[1][0], P[0][1], P[1][1], o0, o1);
+          if constexpr (REST) {
+            mma_16816(x[0], x[1], x[2], x[3], R[0][0], R[1][0], R[0][1], R[1][1], e0, e1);
+            mma_16816(y[0], y[1], y[2], y[3], R[0][0], R[1][0], R[0][1], R[1][1], o0, o1);
+          }
         } else {
           // O^T = V^T P^T: columns of V as the 16 rows of the instruction, so that
           // 8 queries leave no accumulator unused
           float(&x)[4] = O[c][w];
           mma_16816(x[0], x[1], x[2], x[3], e0, o0, e1, o1, P[0][0], P[0][1]);
+          if constexpr (REST) mma_16816(x[0], x[1], x[2], x[3], e0, o0, e1, o1, R[0][0], R[0][1]);
         }
       }
     if (more) load_v(next, V);
@@ -306,7 +329,13 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS, DEPTH>))
     l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
     l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
     if (p == 0) ml[warp][r] = make_float2(m[x], l[x]);
+    if constexpr (!REST) {
+      lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], 1);
+      lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], 2);
+      lr[x] = lr[x] > 0.f ? l[x] / lr[x] : 1.f;
+    }
   }
+  if constexpr (!REST) scale_rows(lr);
 #pragma unroll
   for (int c = 0; c < VC; ++c)
 #pragma unroll

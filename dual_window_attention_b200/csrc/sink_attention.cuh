@@ -85,6 +85,10 @@ __device__ __forceinline__ void mask_scores(float (&s)[N], Word word) {
     for (int i = 0; i < 32; ++i) s[32 * k + i] = (w >> i) & 1u ? s[32 * k + i] : -INFINITY;
   }
 }
+// What the rounding of a pair to `hi` leaves, as bf16.
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
+  return pack_bf16x2(a - bf16lo_to_f32(hi), b - bf16hi_to_f32(hi));
+}
 // The columns of keys k0 .. k0 + 31 that the query at t sees.
 __device__ __forceinline__ uint32_t seen_bits(int t, int k0, int window, int n_sink) {
   return low_bits(t + 1 - k0) & (~low_bits(t - window + 1 - k0) | low_bits(n_sink - k0));

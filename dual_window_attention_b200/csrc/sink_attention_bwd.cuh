@@ -17,8 +17,9 @@
 // (TMEM lane, quarter of the columns).  p stays in registers in 32 bits between the
 // exponential and dS; P and dS are rounded to bf16 as operands of products.  In the sinks'
 // key tile, whose few keys carry a large part of many rows' weight, what that rounding
-// leaves is a second operand, in the columns beside the first: one visit of a row
-// in the dQ kernel, the items of the first key tile in the other.  With it the error of dq,
+// leaves is a second operand, in the columns beside the first: the last visit of a row
+// in the dQ kernel (without sinks too, where it covers windows of one or two tiles), the
+// items of the first key tile in the other.  With it the error of dq,
 // dk and dv is that of their last rounding (0.0017, relative, instead of 0.0021-0.0028).  S and
 // dP have one buffer each, and what alternates is the work: while the element warps
 // form P from S, the tensor cores run the products of dS and the next dP, and while
@@ -159,10 +160,6 @@ __device__ __forceinline__ void ds32(const float (&p)[32], float (&dp)[32], uint
     f2unpack(mul2(f2pack(p[i], p[i + 1]), add2(f2pack(dp[i], dp[i + 1]), nd2)), dp[i], dp[i + 1]);
 }
 
-// What the rounding of a pair to `hi` leaves, as bf16.
-__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t hi) {
-  return pack_bf16x2(a - bf16lo_to_f32(hi), b - bf16hi_to_f32(hi));
-}
 // 32 columns as bf16 over the first half of their own columns, and, where `split`,
 // what that leaves over the second half.
 __device__ __forceinline__ void store_operand(uint32_t taddr, const float (&x)[32], bool split) {
@@ -314,7 +311,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
           for (int kk = 0; kk < 8; ++kk)
             mma_bf16_ts_lh(tmem + C_DQ, tmem + C_DP + (kk >> 1) * 32 + (kk & 1) * 8,
                            kb + ((kk * 2048) >> 4), HI, ID_DQ, (v > 0 || kk > 0) ? 1u : 0u);
-          if (a.n_sink > 0 && v == nv - 1) {  // and what its rounding left
+          if (v == nv - 1) {  // and what its rounding left
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_bf16_ts_lh(tmem + C_DQ, tmem + C_DP + (kk >> 1) * 32 + 16 + (kk & 1) * 8,
@@ -423,7 +420,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         if (qd == 0) rows[128 + r] = split3(row_ok ? exact : 0.f);
       }
       ds32(p, dp, nd2);
-      store_operand(dp_addr, dp, a.n_sink > 0 && v == nv - 1);
+      store_operand(dp_addr, dp, v == nv - 1);
       mbar_arrive(ds_ready);
     }
     if (ok && warp_wait(done, 0, st, abort)) {
@@ -502,7 +499,8 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
   // may be 0: a part without visits
   const int nv = (far ? all : static_cast<int>(static_cast<long long>(all) * (part + 1) / parts)) - cut;
   const int rows_used = a.G * a.tpt;
-  const bool split = kt == 0 && a.n_sink > 0;  // the sinks' tile
+  // the sinks' tile, or the only one (few rows, which average little)
+  const bool split = kt == 0 && (a.n_sink > 0 || a.n_kt == 1);
 
   if (threadIdx.x == 0) {
     for (uint64_t* p = bars; p <= done; ++p) mbar_init(p, (p >= p_ready && p < dp_full) || p == ds_ready ? SINKB_ROWS : 1);

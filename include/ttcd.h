@@ -591,8 +591,8 @@ ttcd_status ttcd_block_decode_next_ex(const void* x_t, const float* beta_t,
  *   workspace  >= ttcd_sink_window_attn_backward_workspace_size(...) bytes,
  *              device, 16-byte aligned; status word first
  * Precision: bf16 tensor-core operands, fp32 sums, statistics and exponentials;
- * P (and dS in the backward) are rounded to bf16 once, as operands; o, dq, dk
- * and dv are rounded to bf16 once, at the end.  delta_t is sum_j p_j dp_j in fp32 for
+ * P (and dS in the backward) are rounded to bf16 once, as operands, where the
+ * sinks are to two bf16 each (16 bits); o, dq, dk and dv are rounded to bf16 once, at the end.  delta_t is sum_j p_j dp_j in fp32 for
  * dk and for the last 128 keys of a row's walk, the sinks among them, and dO_t . o_t
  * (with the rounded o) for the other terms of dq.  K and V (and in the backward Q
  * and d_o) are expected finite: rows that no query of a tile sees are not
@@ -652,7 +652,9 @@ ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const v
  * ascending or beyond total_q) are recorded in the per-device status word
  * (ttcd_get_device_error: TTCD_ERR_INVALID_ARG): such a page counts as zeros
  * and is not written, such a sequence is skipped.  Sequences may share pages
- * that none of them writes.  Precision as ttcd_sink_window_attn.
+ * that none of them writes.  Precision as ttcd_sink_window_attn; sequences of few new
+ * tokens: P as two bf16 throughout (hd 32, 64), or rounded once with the weights' sum
+ * that of the rounded ones (hd 128).
  */
 ttcd_status ttcd_paged_kv_append(const void* qkv, void* q_out, void* k_pages, void* v_pages,
                                  const int* block_table, const int* q_start, const int* kv_len,

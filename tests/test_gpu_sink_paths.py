@@ -179,3 +179,46 @@ def test_a_window_of_any_length_is_causal(ttcd, window):
     want = ttcd.sink_window_attn_backward(q, k, v, o, lse, q, 300, 4)
     got = ttcd.sink_window_attn_backward(q, k, v, o, lse, q, window, 4)
     assert all(torch.equal(a, b) for a, b in zip(want[:3], got[:3]))
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("Hq", [2, 12])
+def test_a_sink_with_most_of_the_weight_is_not_rounded_twice(ttcd, hd, Hq):
+    """Key 0 has almost all of every row's weight p_0.  With weights that are off by
+    r_j, |r_j| <= U, and the sum of the same weights below, the result is off by at most
+    2 U (1 - p_0) |v_0| + 2 U sum_{j > 0} p_j |v_j| (over 1 - U), beside its own rounding
+    U |o| and the 32-bit work W: the rounding of p_0 must not show."""
+    T, window, page = 304, 40, 16
+    g = torch.Generator().manual_seed(hd)
+    q, k, v = (torch.randn(1, T, h, hd, generator=g) for h in (Hq, 1, 1))
+    q *= 0.5
+    q[..., 0] += 6
+    k[:, 0] = 0
+    k[:, 0, :, 0] = 10 * hd ** 0.5 / 6
+    q, k, v = (x.bfloat16() for x in (q, k, v))
+    # the exponential adds 2.8e-6 and 2^-22 of a score (below 24): 0.07 W
+    assert so.score_slack(np64(q), np64(k), hd ** -0.5) <= 0.9 * so.W
+    t, vs = np.arange(T), np.abs(np64(v)[0, :, 0])
+    refs, bounds = [], []
+    for h in range(Hq):
+        ro, _, p, _ = so.attend(np64(q)[0, :, h], np64(k)[0, :, 0], np64(v)[0, :, 0], t, t, window, 1,
+                                hd ** -0.5)
+        assert np.median(p[:, 0]) > 0.99
+        refs.append(ro)
+        others = (1 - p[:, :1]) * vs[:1] + p[:, 1:] @ vs[1:]
+        bounds.append(so.U * np.abs(ro) + 2 * so.U / (1 - so.U) * others + so.W * (p @ vs))
+    ref, bound = np.stack(refs, 1), np.stack(bounds, 1)
+    o, _ = ttcd.sink_window_attn(q.cuda(), k.cuda(), v.cuda(), window, 1)
+    _within(o[0], ref, bound, "dense")
+    # single tokens at every position, over pages that all sequences share
+    k_pages, v_pages = (x[0].view(T // page, page, 1, hd).transpose(1, 2).contiguous().cuda() for x in (k, v))
+    table = torch.arange(T // page, dtype=torch.int32).expand(T, -1).contiguous().cuda()
+    one, _ = ttcd.paged_window_attn(q[0].cuda(), k_pages, v_pages, table,
+                                    torch.arange(T + 1, dtype=torch.int32).cuda(),
+                                    torch.arange(1, T + 1, dtype=torch.int32).cuda(), window, 1, max_q=1)
+    _within(one, ref, bound, "paged")
+    # and one chunk of them all
+    chunk, _ = ttcd.paged_window_attn(q[0].cuda(), k_pages, v_pages, table[:1].contiguous(),
+                                      torch.tensor([0, T], dtype=torch.int32).cuda(),
+                                      torch.tensor([T], dtype=torch.int32).cuda(), window, 1, max_q=T)
+    _within(chunk, ref, bound, "chunk")
