@@ -651,7 +651,8 @@ ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const v
  * (kv_len below the new tokens or above max_pages page_size, q_start not
  * ascending or beyond total_q) are recorded in the per-device status word
  * (ttcd_get_device_error: TTCD_ERR_INVALID_ARG): such a page counts as zeros
- * and is not written, such a sequence is skipped.  Sequences may share pages
+ * and is not written, such a sequence is skipped.  A q_start that does not
+ * ascend may cost other sequences of the call their rows as well.  Sequences may share pages
  * that none of them writes.  Precision as ttcd_sink_window_attn; sequences of few new
  * tokens: P as two bf16 throughout (hd 32, 64), or rounded once with the weights' sum
  * that of the rounded ones (hd 128).

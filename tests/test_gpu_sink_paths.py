@@ -222,3 +222,26 @@ def test_a_sink_with_most_of_the_weight_is_not_rounded_twice(ttcd, hd, Hq):
                                       torch.tensor([0, T], dtype=torch.int32).cuda(),
                                       torch.tensor([T], dtype=torch.int32).cuda(), window, 1, max_q=T)
     _within(chunk, ref, bound, "chunk")
+
+
+def test_more_sequences_than_one_search_step(ttcd):
+    """1100 sequences of none to three new tokens: the write gives the bits that calls of
+    20 sequences give, and the attention is the oracle's through either kernel."""
+    g = torch.Generator().manual_seed(31)
+    new = torch.randint(0, 4, (1100,), generator=g).tolist()
+    lens = [n + int(x) for n, x in zip(new, torch.randint(1, 30, (1100,), generator=g))]
+    b = Batch(lens, new, 2, 1, 64, 16, 12, 2, seed=4)
+    for max_q in (1, 64):
+        b.check(*b.attend(ttcd, lse=True, max_q=max_q))
+    table = torch.arange(b.table.numel(), dtype=torch.int32).view(b.table.shape).cuda()
+    qkv = torch.randn(b.total, 4 * 64, generator=g).bfloat16().cuda()
+    pools = [torch.zeros(table.numel(), 1, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    q = ttcd.paged_kv_append(qkv, *pools[:2], table, b.q_start, b.kv_len, 2)
+    for s in range(0, 1100, 20):
+        at = b.q_start[s:s + 21]
+        lo, hi = at[0].item(), at[-1].item()
+        part = ttcd.paged_kv_append(qkv[lo:hi], *pools[2:], table[s:s + 20], (at - lo).contiguous(),
+                                    b.kv_len[s:s + 20].clone(), 2)
+        assert torch.equal(part, q[lo:hi])
+    assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+    assert pools[0].any() and ttcd.get_device_error()[0] == ttcd.OK
