@@ -26,8 +26,6 @@
 //   warp 1      TMEM owner and MMA issuer; zeroes V rows that no query of the CTA
 //               sees (behind the sequence, before the window), which may hold
 //               anything: 0 times NaN is NaN
-//   warp 2      finds the work unit's sequence (paged)
-//   warp 3      checks the batch's lengths (paged, first CTA)
 //   warps 4..7  softmax of tile A (thread = row), warps 8..11 tile B
 //
 // P is rounded to bf16 as an operand.  The sinks' tile is the last visit, and there what
@@ -269,7 +267,6 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
   uint64_t* drain = o_done + 2;             // 1
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* unit = reinterpret_cast<int*>(tmem_slot + 2);  // paged: sequence, first token, span
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -278,6 +275,43 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
   const int hk = item % a.Hkv;
   const int tpu = a.tpu;
 
+  // The work unit, found by every warp for itself.  A slot without work leaves before the
+  // CTA takes its tensor memory: a batch of many single tokens has mostly such slots.
+  int seq, tok0, q0, n, L;
+  if (PAGED) {
+    const long long capacity = static_cast<long long>(a.max_pages) << a.page_log2;
+    if (blockIdx.x == 0)
+      for (int s = threadIdx.x; s < a.rg.n_seq; s += ATT_THREADS)
+        if (load_span(a.rg, s, capacity).bad) atomicOr(st.err, DEV_ERR_BAD_INDEX);
+    const long long slot = item / a.Hkv;
+    seq = find_seq(a.rg, slot, tpu);
+    SeqSpan sp{0, 0, 0, false};
+    long long t0 = 0;
+    if (seq >= 0) {
+      sp = load_span(a.rg, seq, capacity);
+      t0 = (slot - tile_slot(sp.q0, seq, tpu)) * tpu;
+      if (t0 >= sp.n || sp.n < a.min_q) sp.n = 0;
+    }
+    tok0 = static_cast<int>(t0);
+    q0 = sp.q0;
+    n = sp.n;
+    L = sp.L;
+  } else {  // longest (latest) units first
+    const int u = a.n_units - 1 - item / (a.B * a.Hkv);
+    seq = item / a.Hkv % a.B;
+    tok0 = u * tpu;
+    q0 = seq * a.T;
+    n = L = a.T;
+  }
+  // after the kernel of few rows in the same call, this grid may end only when that
+  // one has
+  auto leave = [&]() {
+    if (PAGED && blockIdx.x == 0) grid_dep_wait();
+  };
+  if (n == 0) {  // no tile here; the same for every CTA of the cluster
+    leave();
+    return;
+  }
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < ATT_KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
@@ -299,58 +333,9 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
     tmem_relinquish();
     tc_fence_before();
   }
-  const long long capacity = static_cast<long long>(a.max_pages) << a.page_log2;
-  if (PAGED) {
-    if (warp == 2) {
-      const long long slot = item / a.Hkv;
-      const int s = find_seq(a.rg, slot, tpu);
-      SeqSpan sp{0, 0, 0, false};
-      int tok = 0;
-      if (s >= 0) {
-        sp = load_span(a.rg, s, capacity);
-        const long long t0 = (slot - tile_slot(sp.q0, s, tpu)) * tpu;
-        if (t0 >= sp.n || sp.n < a.min_q) sp.n = 0;
-        tok = static_cast<int>(t0);
-      }
-      if (lane == 0) {
-        unit[0] = s;
-        unit[1] = tok;
-        unit[2] = sp.q0;
-        unit[3] = sp.n;
-        unit[4] = sp.L;
-      }
-    } else if (warp == 3 && blockIdx.x == 0) {
-      for (int s = lane; s < a.rg.n_seq; s += 32)
-        if (load_span(a.rg, s, capacity).bad) atomicOr(st.err, DEV_ERR_BAD_INDEX);
-    }
-  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int seq, tok0, q0, n, L;
-  if (PAGED) {
-    seq = unit[0];
-    tok0 = unit[1];
-    q0 = unit[2];
-    n = unit[3];
-    L = unit[4];
-  } else {  // longest (latest) units first
-    const int u = a.n_units - 1 - item / (a.B * a.Hkv);
-    seq = item / a.Hkv % a.B;
-    tok0 = u * tpu;
-    q0 = seq * a.T;
-    n = L = a.T;
-  }
-  // after the kernel of few rows in the same call, this grid may end only when that
-  // one has
-  auto leave = [&]() {
-    if (PAGED && blockIdx.x == 0) grid_dep_wait();
-  };
-  if (n == 0) {  // no tile here; the same for every CTA of the cluster
-    leave();
-    if (warp == 1) tmem_dealloc(tmem, 512);
-    return;
-  }
   const SinkVisits vis(L - n + tok0, min(n - tok0, tpu), a.tpt, a.window, a.n_sink);
   const int v0 = static_cast<int>(static_cast<long long>(vis.total) * rank / a.splits);
   const int v1 = static_cast<int>(static_cast<long long>(vis.total) * (rank + 1) / a.splits);
