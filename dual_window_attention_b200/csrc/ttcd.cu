@@ -2810,21 +2810,21 @@ ttcd_status launch_sink_fwd(const Ctx& c, const void* q, const void* k, const vo
   a.min_q = min_q;
   a.scale_log2 = scale * 1.4426950408889634f;
   // Work units of `tiles` query tiles that hold work, as far as it is known here
-  // (paged: sequences of max_q new tokens).  Pairs of tiles share the loads of K and
+  // (paged: sequences of max_q new tokens, whose last units are half full in the mean).  Pairs of tiles share the loads of K and
   // V.  Where they would leave half of the SMs idle, their keys are split over
   // clusters if there are enough; otherwise single tiles (2400 cycles a visit instead
   // of 2900) win.
   auto busy = [&](int tiles) -> long long {
     if (!PAGED) return static_cast<long long>(cdiv(T, tiles * tpt)) * Hkv * B;
     return Hkv * (rg.total_q / (static_cast<long long>(tiles) * tpt) +
-                  std::min(rg.n_seq, rg.total_q / max_q + 1));
+                  (std::min(rg.n_seq, rg.total_q / max_q + 1) + 1) / 2);
   };
   const long long key_tiles =
       (std::min<long long>(static_cast<long long>(window) + 2 * tpt + n_sink,
                            PAGED ? static_cast<long long>(pc.max_pages) << pc.page_log2 : T) +
        ATT_BN - 1) / ATT_BN;
   a.splits = pick_splits(busy(2), c.sms, key_tiles);
-  const int tiles = a.splits == 1 && 2 * busy(2) <= c.sms ? 1 : 2;
+  const int tiles = a.splits == 1 && busy(1) <= c.sms ? 1 : 2;
   a.tpu = tiles * tpt;
   a.n_units = PAGED ? static_cast<int>(tile_slots(rg.total_q, rg.n_seq, a.tpu)) : cdiv(T, a.tpu);
   const long long items = static_cast<long long>(a.n_units) * Hkv * (PAGED ? 1 : B);
