@@ -80,8 +80,9 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const Appe
     const int s = seq_of_row(a.rg, row);
     if (s < 0) continue;
     const SeqSpan sp = load_span(a.rg, s, cap);
-    if (row - sp.q0 >= sp.n) continue;  // padding, or a sequence that cannot be
-    const int p = sp.L - sp.n + row - sp.q0;
+    const int tok = row_token(sp, row);
+    if (tok < 0) continue;  // padding, or a sequence that cannot be
+    const int p = sp.L - sp.n + tok;
     const int id = a.table[static_cast<long long>(s) * a.max_pages + (p >> a.page_log2)];
     const long long kv_row = page_row(id, a.n_pages, a.Hkv, 0, page_size);
     if (kv_row < 0 && lane == 0) atomicOr(err, DEV_ERR_BAD_INDEX);

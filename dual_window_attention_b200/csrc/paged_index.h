@@ -37,6 +37,13 @@ TTCD_HD SeqSpan seq_span(int begin, int end, int kv_len, int total_q, long long 
   return s;
 }
 
+// Which token of its sequence the row `row` >= 0 of the packed queries is; -1 for
+// padding and for the rows of a sequence that is skipped, whose q0 may be any number
+// (row - q0 is formed only where it cannot overflow).
+TTCD_HD int row_token(const SeqSpan& s, int row) {
+  return s.n > 0 && row >= s.q0 && row - s.q0 < s.n ? row - s.q0 : -1;
+}
+
 // Query tiles of tpt tokens.  Sequence s's tiles have the slots
 // tile_slot(q_start[s], s) .. + ceil(n / tpt) - 1; the slots of two sequences
 // never meet, because floor((a + n) / tpt) + 1 >= floor(a / tpt) + ceil(n / tpt),
