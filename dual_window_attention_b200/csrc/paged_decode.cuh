@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(PDEC_THREADS, (PDEC_CTAS<HD, ROWS, DEPTH>))
   constexpr int VC = HD / (8 * VE);             // V chunks per lane and key
   constexpr int VW = VE / 2;                    // words of a V chunk
   constexpr bool REST = HD <= 64;               // P as two operands
-  __shared__ float part[PDEC_WARPS][ROWS][HD + 4];
+  __shared__ __align__(16) float part[PDEC_WARPS][ROWS][HD + 4];  // accessed 16 bytes at a time
   __shared__ float2 ml[PDEC_WARPS][ROWS];       // reference maximum, sum
   __shared__ float2 ml_cta[ROWS];
 
