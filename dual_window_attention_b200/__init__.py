@@ -727,7 +727,10 @@ def _launching(dev: int, stream):
     if at is not None and at.index != dev:
         raise ValueError(f"libttcd: the stream is on {at}, the tensors on cuda:{dev}")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=torch.device("cuda", dev))
+        handle = _stream(stream)
+        # the default stream's handle is 0, and torch makes ExternalStream(0) a stream of its pool
+        stream = (torch.cuda.ExternalStream(handle, device=torch.device("cuda", dev)) if handle
+                  else torch.cuda.default_stream(dev))
     return torch.cuda.stream(stream)
 
 
