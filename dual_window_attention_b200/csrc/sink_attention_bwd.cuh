@@ -131,15 +131,17 @@ __device__ __forceinline__ uint4 split3(float x) {
 }
 
 // p = 2^(s scale_log2 + nl) of 32 scores; nl per pair of columns.  One pair in
-// four on the FMA pipe, as the forward (there a masked score gives 2^-126).
-template <class NL>
+// four on the FMA pipe, as the forward (there a masked score gives 2^-126).  KEEP_NAN:
+// there too NaN stays NaN, for columns that are queries, whose log-sum-exp may be NaN
+// (where rows are, the other columns of such a row show it).
+template <bool KEEP_NAN, class NL>
 __device__ __forceinline__ void probs32(float (&s)[32], float scale_log2, NL nl) {
   const uint64_t sc2 = f2pack(scale_log2, scale_log2);
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     const uint64_t x = fma2(f2pack(s[c], s[c + 1]), sc2, nl(c));
     if (((c >> 1) & 3) == 3) {
-      f2unpack(exp2_poly2_fine(x), s[c], s[c + 1]);
+      f2unpack(exp2_poly2_fine<KEEP_NAN>(x), s[c], s[c + 1]);
     } else {
       float x0, x1;
       f2unpack(x, x0, x1);
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
           k0 + 127 <= t0 && (k0 > t1 - a.window || k0 + 128 <= a.n_sink);
       if (!unmasked)
         mask_scores(p, [&](int) { return seen_bits(t, k0 + 32 * qd, a.window, a.n_sink); });
-      probs32(p, a.scale_log2, [&](int) { return nl2; });
+      probs32<false>(p, a.scale_log2, [&](int) { return nl2; });
       if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }
       float dp[32];
       tmem_ld32f(dp_addr, dp);
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(SINKB_THREADS, 1)
         const int hi = last * a.G - 32 * qd;
         mask_scores(p, [&](int) { return low_bits(hi) & ~low_bits(lo); });
       }
-      probs32(p, a.scale_log2, [](int) { return 0ull; });
+      probs32<true>(p, a.scale_log2, [](int) { return 0ull; });
       store_operand(s_at, p, split);
       mbar_arrive(&p_ready[v % NBS]);
       if (!warp_wait(dp_full, v & 1, st, abort)) { ok = false; break; }

@@ -109,16 +109,30 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// The largest number, or NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // exp2_poly2 with a quartic (relative error 2.8e-6; the same fit): inputs are
-// clamped at -126.
+// clamped at -126.  NaN gives 2^-126, unless KEEP_NAN: then the maximum keeps it, and a
+// last step, x 0 + y, puts it back after the exponent was added to its bits.
+template <bool KEEP_NAN = false>
 __device__ __forceinline__ uint64_t exp2_poly2_fine(uint64_t x) {
   constexpr float SHIFT = 12582912.0f;  // 1.5 * 2^23
   constexpr float C1 = 0.6931241934163351f, C2 = 0.24024098610072953f,
                   C3 = 0.0559064246048171f, C4 = 0.00958285308972204f;
   float x0, x1;
   f2unpack(x, x0, x1);
-  x0 = fmaxf(x0, -126.0f);
-  x1 = fmaxf(x1, -126.0f);
+  x0 = KEEP_NAN ? max_nan(x0, -126.0f) : fmaxf(x0, -126.0f);
+  x1 = KEEP_NAN ? max_nan(x1, -126.0f) : fmaxf(x1, -126.0f);
   const uint64_t xc = f2pack(x0, x1);
   const uint64_t t = add2(xc, f2pack(SHIFT, SHIFT));
   const uint64_t n = add2(t, f2pack(-SHIFT, -SHIFT));
@@ -132,7 +146,8 @@ __device__ __forceinline__ uint64_t exp2_poly2_fine(uint64_t x) {
   f2unpack(t, t0, t1);
   const float r0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
   const float r1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
-  return f2pack(r0, r1);
+  const uint64_t r = f2pack(r0, r1);
+  return KEEP_NAN ? fma2(xc, f2pack(0.f, 0.f), r) : r;
 }
 
 // Four columns of a row merged over the parts of a cluster's CTAs (four parts in
@@ -536,19 +551,21 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
                             (k0 > p_hi - a.window || k0 + ATT_BN <= a.n_sink);
       if (!unmasked)
         mask_scores(s, [&](int k) { return seen_bits(t, k0 + 32 * k, a.window, a.n_sink); });
-      // row maximum as four independent chains (short dependency latency)
+      // row maximum as four independent chains (short dependency latency); a visible
+      // score of NaN or +inf makes it NaN and with it the row, as the softmax does (the
+      // exponentials alone would lose it in the columns of the FMA pipe)
       float mx4[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float m = fmax3(s[32 * q], s[32 * q + 1], s[32 * q + 2]);
+        float m = max_nan(s[32 * q], s[32 * q + 1], s[32 * q + 2]);
 #pragma unroll
-        for (int c = 3; c < 31; c += 2) m = fmax3(m, s[32 * q + c], s[32 * q + c + 1]);
-        mx4[q] = fmaxf(m, s[32 * q + 31]);
+        for (int c = 3; c < 31; c += 2) m = max_nan(m, s[32 * q + c], s[32 * q + c + 1]);
+        mx4[q] = max_nan(m, s[32 * q + 31]);
       }
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      const float m_tile = mx * sl2;
+      const float mx = max_nan(max_nan(mx4[0], mx4[1]), max_nan(mx4[2], mx4[3]));
+      const float m_tile = mx < INFINITY ? mx * sl2 : __int_as_float(0x7fffffff);
       const bool fresh = m_ref == -INFINITY;
-      const bool grow = !fresh && m_tile > m_ref + ATT_RESCALE_THRESHOLD;
+      const bool grow = !fresh && !(m_tile <= m_ref + ATT_RESCALE_THRESHOLD);
       if (__any_sync(0xffffffffu, grow || !ok)) {
         if (!__all_sync(0xffffffffu, ok)) { ok = false; return false; }
         const float m_new = grow ? m_tile : m_ref;
@@ -618,7 +635,9 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       // ---------------------------------------------------------------- epilogue
       if (ok && cnt > 0) {
         __nv_bfloat16* dst = a.o + (static_cast<long long>(row) * a.Hq + head) * HD;
-        tmem_store_row<HD, __nv_bfloat16>(o_addr, 1.f / l, dst, row_ok);
+        // a row whose visible scores are all -inf has no softmax (its l is what masked scores gave)
+        const float inv = m_ref == -INFINITY ? __int_as_float(0x7fffffff) : 1.f / l;
+        tmem_store_row<HD, __nv_bfloat16>(o_addr, inv, dst, row_ok);
         if (row_ok && a.lse) a.lse[lse_at(row, head, t)] = (m_ref + __log2f(l)) * 0.6931471805599453f;
       }
     } else {
@@ -628,8 +647,8 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       asm volatile("bar.sync 1, 256;" ::: "memory");
       const int R = h * 128 + r;
       float2* ml = reinterpret_cast<float2*>(smem + SC::ML_OFF);
-      const bool part = ok && cnt > 0 && l > 0.f;
-      ml[R] = part ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
+      // a row with no visible key here has -inf, and then only a NaN of its l counts
+      ml[R] = ok && cnt > 0 ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
       float* mine = reinterpret_cast<float*>(smem + R * SC::PITCH);
 #pragma unroll
       for (int c = 0; c < HD; c += 32) {

@@ -594,8 +594,9 @@ ttcd_status ttcd_block_decode_next_ex(const void* x_t, const float* beta_t,
  * P (and dS in the backward) are rounded to bf16 once, as operands, where the
  * sinks are to two bf16 each (16 bits); o, dq, dk and dv are rounded to bf16 once, at the end.  delta_t is sum_j p_j dp_j in fp32 for
  * dk and for the last 128 keys of a row's walk, the sinks among them, and dO_t . o_t
- * (with the rounded o) for the other terms of dq.  K and V (and in the backward Q
- * and d_o) are expected finite: rows that no query of a tile sees are not
+ * (with the rounded o) for the other terms of dq.  A score that is NaN or +inf makes the
+ * rows that see its key NaN (o and lse), and no others; one of -inf takes the key out.
+ * V (and in the backward K, Q and d_o) is expected finite: rows that no query of a tile sees are not
  * multiplied, but a non-finite V row also reaches the queries of the same tile
  * of 128 rows whose mask hides it (their weight for it is 0).
  * Timeouts of ttcd_sink_window_attn are recorded in the per-device status word.
