@@ -773,6 +773,14 @@ def _c_int(what: str, name: str, x: int) -> int:
     return x
 
 
+def _c_float(what: str, name: str, x: float) -> float:
+    """A number that a C float holds: one that becomes 0 there would ask for something
+    else (the library refuses those that become infinite)."""
+    if x and not ctypes.c_float(x).value:
+        raise ValueError(f"{what}: {name} {x} is 0 in 32 bits")
+    return x
+
+
 def _window(what: str, x: int) -> int:
     """A window as a C int: one beyond every position hides nothing, like 2^30."""
     return _c_int(what, "window", x if x < 1 << 30 else 1 << 30)
@@ -797,6 +805,7 @@ def sink_window_attn(q, k, v, window: int, n_sink: int, scale: float = 0.0, o=No
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("sink_window_attn: q and k are [B, T, heads, head_dim]")
     window, n_sink = _window(what, window), _c_int(what, "n_sink", n_sink)
+    scale = _c_float(what, "scale", scale)
     B, T, Hq, hd = q.shape
     Hkv = k.shape[2]
     kv, dtype, dev = (B, T, Hkv, hd), q.dtype, q.get_device()
@@ -821,6 +830,7 @@ def sink_window_attn_backward(q, k, v, o, lse, d_o, window: int, n_sink: int, sc
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("sink_window_attn_backward: q and k are [B, T, heads, head_dim]")
     window, n_sink = _window(what, window), _c_int(what, "n_sink", n_sink)
+    scale = _c_float(what, "scale", scale)
     B, T, Hq, hd = q.shape
     Hkv = k.shape[2]
     kv, dev = (B, T, Hkv, hd), q.get_device()
@@ -872,6 +882,7 @@ def paged_kv_append(qkv, k_pages, v_pages, block_table, q_start, kv_len, n_q_hea
     if k_pages.dim() != 4 or qkv.dim() != 2:
         raise ValueError("paged_kv_append: qkv is [total, (Hq + 2 Hkv) head_dim], k_pages "
                          "[n_pages, Hkv, page_size, head_dim]")
+    rope_theta = _c_float(what, "rope_theta", rope_theta)
     _, Hkv, _, hd = k_pages.shape
     total, dtype, dev = qkv.shape[0], k_pages.dtype, qkv.get_device()
     n_seq, n_pages, page_size, max_pages, Hkv = _paged(
@@ -902,6 +913,7 @@ def paged_window_attn(q, k_pages, v_pages, block_table, q_start, kv_len, window:
     if q.dim() != 3:
         raise ValueError("paged_window_attn: q is [total, Hq, head_dim]")
     window, n_sink = _window(what, window), _c_int(what, "n_sink", n_sink)
+    scale = _c_float(what, "scale", scale)
     max_q = _c_int(what, "max_q", max_q)
     total, Hq, hd = q.shape
     given = lse if isinstance(lse, torch.Tensor) else None

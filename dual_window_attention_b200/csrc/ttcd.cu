@@ -2688,7 +2688,7 @@ constexpr int kMaxSinks = 128;  // the sinks lie in the first tile of 128 keys
 ttcd_status check_sink_shape(int Hq, int Hkv, int hd, int window, int n_sink, float scale,
                              ttcd_dtype dtype) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || window < 1 || n_sink < 0 || !(scale >= 0.f) ||
-      !std::isfinite(scale))
+      !std::isfinite(scale * 1.4426950408889634f))  // the kernels' base-2 units
     return TTCD_ERR_INVALID_ARG;
   if (dtype != TTCD_BF16) return dtype == TTCD_F32 ? TTCD_ERR_UNSUPPORTED : TTCD_ERR_INVALID_ARG;
   if (hd != 32 && hd != 64 && hd != 128) return TTCD_ERR_UNSUPPORTED;
@@ -3114,7 +3114,7 @@ ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const v
                                            void* dq, void* dk, void* dv, int B, int T, int Hq,
                                            int Hkv, int hd, int window, int n_sink, float scale,
                                            void* workspace, size_t ws_bytes, void* stream) {
-  if (!(scale >= 0.f) || !std::isfinite(scale)) return TTCD_ERR_INVALID_ARG;
+  if (!(scale >= 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return TTCD_ERR_INVALID_ARG;
   if (scale > 0.f && scale < 1e-30f) return TTCD_ERR_UNSUPPORTED;  // lse / scale is formed
   TTCD_TRY(check_sink_bwd(B, T, Hq, Hkv, hd, window, n_sink));
   const void* need[] = {q, k, v, o, lse, d_o, dq, dk, dv, workspace};
