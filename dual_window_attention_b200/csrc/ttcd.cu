@@ -2921,23 +2921,22 @@ ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& p
   // Two tiles in flight per warp on fewer CTAs, unless that leaves half of the warps
   // or less: 256 units of 8200 keys 154 us instead of 174, 512 298 instead of 304,
   // but 192 140 instead of 120 (one CTA each instead of two).
-  const long long held1 = static_cast<long long>(c.sms) * (PDEC_CTAS<HD, ROWS, 1>);
-  const int s1 = pick_unit_splits(units, held1, keys);
-  a.splits = s1;
-  bool deep = false;
-  if constexpr (ROWS == 8) {
-    const long long held2 = static_cast<long long>(c.sms) * (PDEC_CTAS<HD, ROWS, 2>);
-    const int s2 = pick_unit_splits(units, held2, keys);
-    deep = !(units <= held1 && (units > held2 || s1 >= 2 * s2));
-    if (deep) a.splits = s2;
-  }
+  // (head_dim 32 holds as many CTAs either way: always two.)
+  constexpr int CTAS1 = PDEC_CTAS<HD, ROWS, 1>, CTAS2 = PDEC_CTAS<HD, ROWS, 2>;
+  constexpr bool ONE = ROWS == 16 || CTAS1 > CTAS2, TWO = ROWS == 8;  // variants that calls reach
+  const long long held1 = static_cast<long long>(c.sms) * CTAS1;
+  const long long held2 = static_cast<long long>(c.sms) * CTAS2;
+  const int s1 = pick_unit_splits(units, held1, keys), s2 = pick_unit_splits(units, held2, keys);
+  const bool deep = TWO && !(ONE && units <= held1 && (units > held2 || s1 >= 2 * s2));
+  a.splits = deep ? s2 : s1;
   const long long slots =
       rg.n_seq + (beside ? 0ll : static_cast<long long>(extra_slot(rg.total_q, a.tpt)));
   const long long grid = slots * pc.Hkv * a.splits;
   if (grid >= (1ll << 31)) return TTCD_ERR_UNSUPPORTED;
-  if constexpr (ROWS == 8)
+  if constexpr (TWO)
     if (deep) return launch_paged_units<HD, ROWS, 2>(c, a, grid);
-  return launch_paged_units<HD, ROWS, 1>(c, a, grid);
+  if constexpr (ONE) return launch_paged_units<HD, ROWS, 1>(c, a, grid);
+  return TTCD_ERR_CUDA;  // not reached
 }
 
 // The paged attention.  A sequence whose new tokens times group heads fill at
