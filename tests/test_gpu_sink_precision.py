@@ -45,7 +45,7 @@ def test_lse_keeps_32_bit_quality(ttcd, hd):
     per visit, 2^-24 each and two visits at most: 2.3e-6; 2^-22 of a hardware
     exponential; two ulps of the hardware logarithm (below 8): 2^-20 ln 2; a few 2^-24 of
     scores and sums below 8: 2^-21.  Together 6.5e-6."""
-    T, y = 256, -0.46875  # of a power of two: where a cubic's error is largest
+    T, y = 256, -0.34375  # the exponent: near the largest error of the cubic, 1.0e-4
     scale = float(np.float32(np.log(2)))
     q = torch.zeros(1, T, 2, hd, dtype=torch.bfloat16)
     q[..., 0] = 1
