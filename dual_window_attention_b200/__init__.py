@@ -925,7 +925,7 @@ def paged_window_attn(q, k_pages, v_pages, block_table, q_start, kv_len, window:
     with _launching(dev, stream):
         o = torch.empty_like(q) if o is None else o
         ls = given
-        if ls is None and lse is True:
+        if ls is None and lse:
             ls = torch.empty(Hq, total, device=q.device, dtype=_F32)
         _check(lib.ttcd_paged_window_attn(_at(q), _at(k_pages), _at(v_pages), _at(block_table),
                                           _at(q_start), _at(kv_len), _at(o), _at(ls), n_seq, total,
