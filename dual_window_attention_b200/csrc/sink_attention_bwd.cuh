@@ -131,8 +131,7 @@ __device__ __forceinline__ uint4 split3(float x) {
 }
 
 // p = 2^(s scale_log2 + nl) of 32 scores; nl per pair of columns.  One pair in
-// four on the FMA pipe, as the forward (there a masked score gives 2^-126).  KEEP_NAN:
-// there too NaN stays NaN, for columns that are queries, whose log-sum-exp may be NaN
+// four on the FMA pipe, as the forward.  KEEP_NAN: there too NaN stays NaN, for columns that are queries, whose log-sum-exp may be NaN
 // (where rows are, the other columns of such a row show it).
 template <bool KEEP_NAN, class NL>
 __device__ __forceinline__ void probs32(float (&s)[32], float scale_log2, NL nl) {

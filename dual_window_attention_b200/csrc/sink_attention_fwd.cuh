@@ -122,8 +122,11 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
 }
 
 // exp2_poly2 with a quartic (relative error 2.8e-6; the same fit): inputs are
-// clamped at -126.  NaN gives 2^-126, unless KEEP_NAN: then the maximum keeps it, and a
-// last step, x 0 + y, puts it back after the exponent was added to its bits.
+// clamped at -127, where the polynomial is 1 and its exponent becomes that of 0, so that
+// a masked score weighs exactly 0 (2^-126 of a large hidden value would show); between
+// -127 and -126 results are some number below 2^-126.  NaN gives 0, unless KEEP_NAN: then
+// the maximum keeps it, and a last step, x 0 + y, puts it back after the exponent was
+// added to its bits.
 template <bool KEEP_NAN = false>
 __device__ __forceinline__ uint64_t exp2_poly2_fine(uint64_t x) {
   constexpr float SHIFT = 12582912.0f;  // 1.5 * 2^23
@@ -131,8 +134,8 @@ __device__ __forceinline__ uint64_t exp2_poly2_fine(uint64_t x) {
                   C3 = 0.0559064246048171f, C4 = 0.00958285308972204f;
   float x0, x1;
   f2unpack(x, x0, x1);
-  x0 = KEEP_NAN ? max_nan(x0, -126.0f) : fmaxf(x0, -126.0f);
-  x1 = KEEP_NAN ? max_nan(x1, -126.0f) : fmaxf(x1, -126.0f);
+  x0 = KEEP_NAN ? max_nan(x0, -127.0f) : fmaxf(x0, -127.0f);
+  x1 = KEEP_NAN ? max_nan(x1, -127.0f) : fmaxf(x1, -127.0f);
   const uint64_t xc = f2pack(x0, x1);
   const uint64_t t = add2(xc, f2pack(SHIFT, SHIFT));
   const uint64_t n = add2(t, f2pack(-SHIFT, -SHIFT));
@@ -248,7 +251,7 @@ struct SinkVisits {
 __device__ __forceinline__ uint64_t prob2(float s0, float s1, uint64_t scale2, uint64_t offset2,
                                           int column) {
   const uint64_t x = fma2(f2pack(s0, s1), scale2, offset2);
-  // one pair in four on the FMA pipe (a masked score: 2^-126)
+  // one pair in four on the FMA pipe
   if (((column >> 1) & 3) == 3) return exp2_poly2_fine(x);
   float x0, x1;
   f2unpack(x, x0, x1);
@@ -635,9 +638,8 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
       // ---------------------------------------------------------------- epilogue
       if (ok && cnt > 0) {
         __nv_bfloat16* dst = a.o + (static_cast<long long>(row) * a.Hq + head) * HD;
-        // a row whose visible scores are all -inf has no softmax (its l is what masked scores gave)
-        const float inv = m_ref == -INFINITY ? __int_as_float(0x7fffffff) : 1.f / l;
-        tmem_store_row<HD, __nv_bfloat16>(o_addr, inv, dst, row_ok);
+        // (a row whose visible scores are all -inf has no softmax: l and O are 0, their quotient NaN)
+        tmem_store_row<HD, __nv_bfloat16>(o_addr, 1.f / l, dst, row_ok);
         if (row_ok && a.lse) a.lse[lse_at(row, head, t)] = (m_ref + __log2f(l)) * 0.6931471805599453f;
       }
     } else {

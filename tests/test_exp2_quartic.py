@@ -49,19 +49,32 @@ def test_committed_quartic_relative_error():
     assert 2.5e-6 < err.max() <= 2.85e-6  # the minimax level
 
 
-def test_restated_range_reduction():
+def restated(x):
     """Clamp, shifter rounding, Horner, exponent add, in fp32."""
+    c = committed_coefficients().astype(np.float32)
+    shift = np.float32(12582912.0)
+    xc = np.maximum(x, np.float32(-127.0))
+    t = (xc + shift).astype(np.float32)
+    fr = (xc - (t - shift)).astype(np.float32)
+    p = np.full_like(xc, c[3])
+    for y in (c[2], c[1], c[0], np.float32(1.0)):  # each step rounded once, as a fused one is
+        p = (p.astype(np.float64) * fr + y).astype(np.float32)
+    return (p.view(np.int32) + (t.view(np.int32) << 23)).view(np.float32)
+
+
+def test_restated_range_reduction():
     g = np.random.default_rng(0)
     x = np.concatenate([np.linspace(-126.0, 8.0, 200001), g.uniform(-126.0, 8.0, 100000),
                         np.arange(-126, 9) + 0.5, np.arange(-126, 9)]).astype(np.float32)
-    c = committed_coefficients().astype(np.float32)
-    shift = np.float32(12582912.0)
-    t = (np.maximum(x, np.float32(-126.0)) + shift).astype(np.float32)
-    fr = (x - (t - shift)).astype(np.float32)
-    p = np.full_like(x, c[3])
-    for y in (c[2], c[1], c[0], np.float32(1.0)):  # each step rounded once, as a fused one is
-        p = (p.astype(np.float64) * fr + y).astype(np.float32)
-    y = (p.view(np.int32) + (t.view(np.int32) << 23)).view(np.float32)
-    # at x = -126 and just above, results of less than 2^-126 have lost bits
-    err = np.abs(y / 2.0 ** x.astype(np.float64) - 1.0)[x >= -125]
+    # below -125, results of less than 2^-126 have lost bits
+    err = np.abs(restated(x) / 2.0 ** x.astype(np.float64) - 1.0)[x >= -125]
     assert err.max() <= BOUND, err.max()
+
+
+def test_restated_ends():
+    """Masked scores weigh exactly 0, and what is near them nothing that is not tiny."""
+    np.testing.assert_array_equal(restated(np.array([-np.inf, -1e30, -127.5, -127.0], np.float32)), 0.0)
+    y = restated(np.linspace(-127.0, -125.5, 300001).astype(np.float32))
+    assert (y >= 0).all() and y.max() <= 1.5 * 2.0 ** -126
+    with open(SRC) as f:
+        assert f.read().count("-127.0f") == 4  # the clamp of this restatement
