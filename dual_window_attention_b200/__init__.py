@@ -799,6 +799,8 @@ def sink_window_attn(q, k, v, window: int, n_sink: int, scale: float = 0.0, o=No
     """Sliding-window attention whose first ``n_sink`` tokens stay visible: the
     query at t sees key j iff j <= t and (j > t - window or j < n_sink).
     q [B, T, Hq, hd], k and v [B, T, Hkv, hd] bf16, hd 32, 64 or 128.
+    The outputs carry no autograd graph, as everywhere in this package: gradients
+    come from ``sink_window_attn_backward``.
     Returns (o, lse [B, Hq, T] or None)."""
     what = "sink_window_attn"
     lib = load_library()
@@ -906,7 +908,7 @@ def paged_window_attn(q, k_pages, v_pages, block_table, q_start, kv_len, window:
     """Attention of new tokens' queries q [total, Hq, hd] over a paged cache, with
     the mask of ``sink_window_attn`` at the tokens' positions; their own k and v
     are in the cache already (``paged_kv_append``).  ``max_q``: about the most new
-    tokens of any sequence (it chooses the kernels).  ``lse``: True, or a tensor
+    tokens of any sequence (it chooses the kernels).  ``lse``: true, or a tensor
     [Hq, total] to write.  Returns (o, lse or None)."""
     what = "paged_window_attn"
     lib = load_library()

@@ -15,8 +15,8 @@
 // access).  One warp per token and no barrier of the block: lane l forms
 // the angles l and l + 32 and hands them on through shared memory of its warp; then each
 // lane keeps the 8 angles of its chunk for all the heads, whose loads go out four
-// at a time before the first is used.  17416 tokens of 32 heads of 128: 43.6 us, 6.5
-// TB/s (one block per token with its barriers: 94); 8 tokens: 4.1 us, a chain of
+// at a time before the first is used.  17416 tokens of 32 heads of 128: 47 us, 6.0
+// TB/s (one block per token with its barriers: 94); 8 tokens: 3.5 us captured, a chain of
 // four loads.
 #pragma once
 #include "sink_attention.cuh"

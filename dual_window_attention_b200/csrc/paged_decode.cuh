@@ -19,9 +19,11 @@
 // The 4 warps of a CTA and the CTAs of a cluster share a unit's tiles and merge
 // their (m, l, O) through shared memory, then distributed shared memory.
 //
-// 64 sequences of 8200 keys, 8 heads of 128: 314 us, 6.5 TB/s (the tiled kernel 484);
-// one of them: 15 us, of which the loads of a warp's 8 tiles are half and the rest
-// the chain lengths -> page -> keys and the merge.
+// 64 sequences that see 498721 keys together, 8 heads of 128: 332 us, 6.2 TB/s.  One of
+// 8196 keys: 16.4 us a call, 13.7 captured, its K and V in L2; its 8 units in clusters of
+// 16 are 128 CTAs of 4 warps, so 20 SMs stay empty and a warp walks 8 tiles, two in
+// flight.  Those four rounds of memory latency are half of the time, the rest the chain
+// lengths -> page -> keys and the merge.
 //
 // Softmax as in the tiled kernel: base-2 units, the reference maximum of a row is
 // moved only when a score exceeds it by 2^8.  P becomes a bf16 operand, and the rounding

@@ -50,8 +50,9 @@
 //   dK/dV  128: 2910 (P 1090, then dV and the next S^T 1100 and 270 of hand-overs beside
 //          dS; 2176 of products); 64: 2200 (products with 64 columns take as long as
 //          with 128: 1664)
-// 32768 tokens, 16 / 8 heads of 128, window 8192: 2.12 and 2.82 ms alone (the
-// forward 1.6); 16384, 15 / 5 of 64, window 4096: 0.43 and 0.49 ms.
+// 32768 tokens, 16 / 8 heads of 128, window 8192: 2.30 and 2.93 ms after idling (the
+// forward 1.57), 2.55 and 3.21 (1.83) one step after another under the power cap; 16384,
+// 15 / 5 of 64, window 4096: 0.48 and 0.49 (0.36) ms, a whole step 1.44 among others.
 // Measured and not kept: 8 element warps 2-3 % slower; two issuing warps at head_dim
 // 128 2.41 and 3.36 ms (the products interleave and each takes twice as long).
 #pragma once

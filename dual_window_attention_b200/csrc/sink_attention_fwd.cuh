@@ -43,8 +43,9 @@
 //                 of hand-overs; the tensor cores work 2048 of them
 //   head_dim 64   2860: S to P 1850 (the two tiles' softmax overlap), products and
 //                 hand-overs 1010; P V with 64 columns takes as long as with 128
-// 65536 tokens, 16 / 8 heads of 128, window 8192: 3.42 ms alone, 3.5-3.9 under the power
-// cap (2.5 ms at the measured cuBLAS rate); 16384, 15 / 5 of 64, window 4096: 0.37 ms.
+// 65536 tokens, 16 / 8 heads of 128, window 8192: 3.36 ms after idling, 3.9-4.0 one call
+// after another under the power cap (2.5 ms at the measured cuBLAS rate); 16384, 15 / 5 of
+// 64, window 4096: 0.36 and 0.37 ms.
 // Measured and not kept (0.37 ms as the base): two threads per row (16 softmax
 // warps) 0.44; visits of 64 or 96 keys with two score buffers and one or two issuing
 // warps 0.40-0.48; a third score buffer at head_dim 64 0.38; turns at the exponentials

@@ -2887,9 +2887,12 @@ ttcd_status launch_paged_units(const Ctx& c, const PagedDecodeArgs& a, long long
 // Clusters of `splits` CTAs per unit: as many as the GPU holds at once, with a tile
 // of 16 keys at least for each warp; or, where the units alone are more, enough for
 // four waves (so that the last one is a small part) of 2048 keys each at least.
-// 120 units of 4100 keys (head_dim 64) with 2, 4, 8 CTAs: 39, 26.7, 31 us; 128 of
-// 8200 (128) 97, 114, 100; 512 of 8200 with 1, 2, 4, 8, 16: 411, 352, 318, 348, 433;
-// 800 of 2052 (64) with 1, 2, 4: 70, 82, 98.
+// Captured, with a cold L2 and about 7 us of events and launch in each figure:
+// 120 units of 4100 keys (head_dim 64) with 2, 4, 8 CTAs: 45, 33, 39 us; 128 of 8196
+// (128) 96, 102, 113; 512 of 7793 in the mean (64 sequences of ragged lengths) with 1, 2,
+// 4, 8, 16 and one tile in flight per warp 440, 375, 340, 371, 455, with two, which they
+// take, 332, 356, 340, 377, 543; 512 of 8196 each 461, 385, 352, 389, 477 and 338, 363, 379,
+// 410, 557 (there 1 would be better than this rule's 4); 800 of 2052 (64) with 1, 2, 4: 82, 94, 111.
 int pick_unit_splits(long long units, long long held, long long keys) {
   const long long most =
       std::min(16ll, units <= held ? keys / (16 * PDEC_WARPS) : keys / 2048);
@@ -2919,8 +2922,8 @@ ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& p
   const long long keys = std::min<long long>(static_cast<long long>(window) + a.tpt + n_sink,
                                              static_cast<long long>(pc.max_pages) << pc.page_log2);
   // Two tiles in flight per warp on fewer CTAs, unless that leaves half of the warps
-  // or less: 256 units of 8200 keys 154 us instead of 174, 512 298 instead of 304,
-  // but 192 140 instead of 120 (one CTA each instead of two).
+  // or less: 128 units of 8196 keys 96 us instead of 107, 256 176 instead of 195, but 192
+  // 174 instead of 137 (one CTA each instead of two).
   // (head_dim 32 holds as many CTAs either way: always two.)
   constexpr int CTAS1 = PDEC_CTAS<HD, ROWS, 1>, CTAS2 = PDEC_CTAS<HD, ROWS, 2>;
   constexpr bool ONE = ROWS == 16 || CTAS1 > CTAS2, TWO = ROWS == 8;  // variants that calls reach
@@ -2941,8 +2944,11 @@ ttcd_status launch_paged_decode(const Ctx& c, const void* q, const PagedCache& p
 
 // The paged attention.  A sequence whose new tokens times group heads fill at
 // most one unit of 16 rows (8 for groups of up to 8) is read by the kernel of few
-// rows, others by the tiled kernel; a batch of both takes both kernels, side by
-// side.  Groups of more than 16 heads fill the tiles of the latter with one token.
+// rows, others by the tiled kernel; a batch of both takes both kernels.  The tiled one is
+// launched programmatically, but its CTA takes all of an SM's registers, so each starts
+// on an SM that the kernel of few rows has left (26 sequences of which 2 bring chunks,
+// 15 / 5 heads of 64: 72 us, of which the kernel of few rows 29).
+// Groups of more than 16 heads fill the tiles of the latter with one token.
 template <int HD>
 ttcd_status launch_paged(const Ctx& c, const void* q, const PagedCache& pc, const Ragged& rg,
                          void* o, float* lse, int max_q, int Hq, int window, int n_sink,

@@ -577,7 +577,7 @@ ttcd_status ttcd_block_decode_next_ex(const void* x_t, const float* beta_t,
  *   k, v       [B, T, Hkv, hd] bf16, device
  *   o          [B, T, Hq, hd]  bf16, device, written
  *   lse        [B, Hq, T] fp32 natural-log log-sum-exp, device, nullable
- *   scale      softmax scale; 0 => 1/sqrt(hd)
+ *   scale      softmax scale; 0 => 1/sqrt(hd); scaled scores are expected below 2^30
  *   dtype      must be TTCD_BF16 (TTCD_F32 -> TTCD_ERR_UNSUPPORTED)
  * ttcd_sink_window_attn_backward: its vector-Jacobian product for dL/do = d_o,
  *   with the formulas of ttcd_dual_window_attn_backward; hd 64 or 128 (32:
@@ -592,13 +592,15 @@ ttcd_status ttcd_block_decode_next_ex(const void* x_t, const float* beta_t,
  *              device, 16-byte aligned; status word first
  * Precision: bf16 tensor-core operands, fp32 sums, statistics and exponentials;
  * P (and dS in the backward) are rounded to bf16 once, as operands, where the
- * sinks are to two bf16 each (16 bits); o, dq, dk and dv are rounded to bf16 once, at the end.  delta_t is sum_j p_j dp_j in fp32 for
- * dk and for the last 128 keys of a row's walk, the sinks among them, and dO_t . o_t
- * (with the rounded o) for the other terms of dq.  A score that is NaN or +inf makes the
- * rows that see its key NaN (o and lse), and no others; one of -inf takes the key out.
- * V (and in the backward K, Q and d_o) is expected finite: rows that no query of a tile sees are not
- * multiplied, but a non-finite V row also reaches the queries of the same tile
- * of 128 rows whose mask hides it (their weight for it is 0).
+ * sinks are to two bf16 each (16 bits); o, dq, dk and dv are rounded to bf16 once,
+ * at the end.  delta_t is sum_j p_j dp_j in fp32 for dk and for the last 128 keys
+ * of a row's walk, the sinks among them, and dO_t . o_t (with the rounded o) for
+ * the other terms of dq.  What the mask hides weighs exactly 0.  A score that is
+ * NaN or +inf makes the rows that see its key NaN (o and lse), and no others; one
+ * of -inf takes the key out.
+ * V (and in the backward K, Q and d_o) is expected finite: rows that no query of a
+ * tile sees are not multiplied, but a non-finite V row also reaches the queries of
+ * the same tile of 128 rows whose mask hides it (0 times infinity).
  * Timeouts of ttcd_sink_window_attn are recorded in the per-device status word.
  */
 ttcd_status ttcd_sink_window_attn(const void* q, const void* k, const void* v, void* o,
@@ -653,8 +655,9 @@ ttcd_status ttcd_sink_window_attn_backward(const void* q, const void* k, const v
  * ascending or beyond total_q) are recorded in the per-device status word
  * (ttcd_get_device_error: TTCD_ERR_INVALID_ARG): such a page counts as zeros
  * and is not written, such a sequence is skipped.  A q_start that does not
- * ascend may cost other sequences of the call their rows as well.  Sequences may share pages
- * that none of them writes.  Precision as ttcd_sink_window_attn; sequences of few new
+ * ascend may cost other sequences of the call their rows as well.  Sequences may
+ * share pages that none of them writes, and a page that a call writes stands in one
+ * place of the table.  Precision as ttcd_sink_window_attn; sequences of few new
  * tokens: P as two bf16 throughout (hd 32, 64), or rounded once with the weights' sum
  * that of the rounded ones (hd 128).
  */
